@@ -28,7 +28,14 @@ EXPORTS = ["csa_version", "csa_last_error", "csa_workspace_bytes", "hca_compress
            "lightning_index_topk_static", "csa_rope_yarn", "hca_prefill_chunk",
            "csa_decode_step", "hca_decode_step", "grouped_out_proj",
            "grouped_out_proj_workspace_bytes", "csa_shard_candidates", "csa_merge_candidates",
-           "sparse_mqa_partials", "mqa_merge_partials", "csa_copy_async", "csa_copy_rows_async"]
+           "sparse_mqa_partials", "mqa_merge_partials", "csa_copy_async", "csa_copy_rows_async",
+           "mxfp4_row_bytes", "mxfp4_cache_write", "mxfp4_cache_read", "hca_compress_mxfp4",
+           "csa_compress_mxfp4", "sparse_mqa_decode_mxfp4", "dense_mqa_decode_mxfp4",
+           "csa_prefill_chunk_mxfp4", "hca_prefill_chunk_mxfp4", "csa_decode_step_mxfp4",
+           "hca_decode_step_mxfp4"]
+# Entry points that return a size, not a status.
+_SIZES = ("csa_version", "csa_last_error", "csa_workspace_bytes",
+          "grouped_out_proj_workspace_bytes", "mxfp4_row_bytes")
 
 
 class CsaError(RuntimeError):
@@ -103,8 +110,16 @@ def _declare(L):
     L.mqa_merge_partials.argtypes = [P, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     L.csa_copy_async.argtypes = [vp, vp, sz, vp]
     L.csa_copy_rows_async.argtypes = [vp, sz, vp, sz, sz, sz, vp]
-    for name in EXPORTS[3:]:
-        if name != "grouped_out_proj_workspace_bytes":
+    # The calls on a 4-bit cache take the arguments of the bf16 ones.
+    for name in EXPORTS:
+        if name.endswith("_mxfp4") and name[:-6] in EXPORTS and name != "grouped_out_proj_mxfp4":
+            getattr(L, name).argtypes = getattr(L, name[:-6]).argtypes
+    L.mxfp4_row_bytes.argtypes = [i32]
+    L.mxfp4_row_bytes.restype = sz
+    L.mxfp4_cache_write.argtypes = [P, vp, i64, i64, vp, vp, vp, i64, vp, vp]
+    L.mxfp4_cache_read.argtypes = [P, vp, i64, vp, vp, vp, i64, vp, vp, vp]
+    for name in EXPORTS:
+        if name not in _SIZES:
             getattr(L, name).restype = i32
 
 
@@ -286,8 +301,8 @@ def csa_decode_step(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos
 
 
 class CsaDecodeStep:
-    """csa_decode_step for a fixed set of sequences: the arguments that stay
-    the same from step to step (token buffers, caches, weights, sink and
+    """csa_decode_step (or, with a uint8 cache, csa_decode_step_mxfp4) for a
+    fixed set of sequences: the arguments that stay the same from step to step (token buffers, caches, weights, sink and
     gains, the selection outputs, workspace and status word) are checked and
     converted once; each call passes the step's positions, queries and
     outputs.  Same C entry point and the same device-side work as
@@ -296,7 +311,8 @@ class CsaDecodeStep:
     def __init__(self, p, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv_c, idx_key,
                  idx_scale, sink, topk_idx, topk_cnt, ws, gamma_q=None, gamma_kv=None,
                  dev_status=None):
-        self._fn = lib().csa_decode_step
+        self._fn = (lib().csa_decode_step_mxfp4 if _is_mxfp4(p, kv_c, kv_tok)
+                    else lib().csa_decode_step)
         self._keep = (p, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv_c, idx_key,
                       idx_scale, sink, topk_idx, topk_cnt, ws, gamma_q, gamma_kv, dev_status)
         self._head = (C.byref(p),)
@@ -326,11 +342,13 @@ class CsaDecodeStep:
 
 
 class HcaDecodeStep:
-    """hca_decode_step for a fixed set of sequences (see CsaDecodeStep)."""
+    """hca_decode_step (or, with a uint8 cache, hca_decode_step_mxfp4) for a
+    fixed set of sequences (see CsaDecodeStep)."""
 
     def __init__(self, p, kv_tok, w_s, b_pos, gamma, kv_c, sink, ws, gamma_q=None, gamma_kv=None,
                  dev_status=None):
-        self._fn = lib().hca_decode_step
+        self._fn = (lib().hca_decode_step_mxfp4 if _is_mxfp4(p, kv_c, kv_tok)
+                    else lib().hca_decode_step)
         self._keep = (p, kv_tok, w_s, b_pos, gamma, kv_c, sink, ws, gamma_q, gamma_kv, dev_status)
         self._head = (C.byref(p),)
         self._mid = (_ptr(kv_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos), _ptr(gamma),
@@ -432,6 +450,218 @@ def grouped_out_proj(o, w_g, w_o, z, y=None, ws=None, dev_status=None, stream=No
     _check(lib().grouped_out_proj(T, H, D, g, d_g, d_model, _ptr(o), _ptr(w_g), _ptr(w_o),
                                   _ptr(y), _ptr(z), _ptr(ws), ws.numel() * ws.element_size(),
                                   _ptr(dev_status), _stream(stream)))
+
+
+# -------------------------------------------------------------- 4-bit (MXFP4) cache --
+def mxfp4_row_bytes(d):
+    """Bytes of a 4-bit cache row of d values (d/2 of codes, d/32 of scales,
+    padded to 16)."""
+    n = lib().mxfp4_row_bytes(d)
+    if n == 0:
+        raise CsaError(2, lib().csa_last_error().decode())
+    return n
+
+
+def mxfp4_cache(p, N_cap, device=None):
+    """An empty (all zero) 4-bit cache [B, N_cap, row bytes] for these params."""
+    return torch.zeros(p.B, N_cap, mxfp4_row_bytes(p.d), dtype=torch.uint8,
+                       device=device or torch.cuda.current_device())
+
+
+def _need(t, name, dtype, *shape):
+    """Pointer of a tensor that must have this dtype and shape (None: any
+    length) and sit on the current device; None passes."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
+    if t.dtype != dtype or t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("*" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must be {dtype} [{want}], not {t.dtype} {list(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return _ptr(t)
+
+
+def _must(t, name, dtype, *shape):
+    """_need for a tensor whose shape the call itself reads."""
+    if t is None:
+        raise TypeError(f"{name}: expected a torch.Tensor, got None")
+    return _need(t, name, dtype, *shape)
+
+
+def _need_cache(p, kv4):
+    return _must(kv4, "kv4", torch.uint8, p.B, None, mxfp4_row_bytes(p.d))
+
+
+def _is_mxfp4(p, kv_c, kv_tok):
+    if kv_c.dtype != torch.uint8:
+        return False
+    _need_cache(p, kv_c)
+    _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d)
+    return True
+
+
+def _ws(ws):
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
+    """Quantises rows [B, n, d] (bf16; each sequence's rows contiguous) into
+    entries first_entry[b] + i, i < count[b], of kv4."""
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 3 or rows.dtype != torch.bfloat16 or \
+            rows.shape[0] != p.B or rows.shape[2] != p.d:
+        raise ValueError(f"rows must be bfloat16 [{p.B}, n, {p.d}]")
+    n = rows.shape[1]
+    if n and not rows[0].is_contiguous():
+        raise ValueError("each sequence's rows must be contiguous")
+    if not rows.is_cuda or rows.device.index != torch.cuda.current_device():
+        raise ValueError("rows must be on the current CUDA device")
+    stride = rows.stride(0) if p.B > 1 else n * p.d
+    _check(lib().mxfp4_cache_write(
+        C.byref(p), C.c_void_p(rows.data_ptr()), stride, n,
+        _need(first_entry, "first_entry", torch.int64, p.B), _need(count, "count", torch.int64, p.B),
+        _need_cache(p, kv4), kv4.shape[1], _need(dev_status, "dev_status", torch.int32, 1),
+        _stream(stream)))
+
+
+def mxfp4_cache_read(p, kv4, rows, idx=None, first_entry=None, count=None, dev_status=None,
+                     stream=None):
+    """The values of entries idx[b, i] (int32, -1 skipped) or first_entry[b] + i,
+    i < count[b], of kv4 into rows [B, n, d] (bf16)."""
+    rp = _must(rows, "rows", torch.bfloat16, p.B, None, p.d)
+    n = rows.shape[1]
+    _check(lib().mxfp4_cache_read(
+        C.byref(p), _need_cache(p, kv4), kv4.shape[1], _need(idx, "idx", torch.int32, p.B, n),
+        _need(first_entry, "first_entry", torch.int64, p.B), _need(count, "count", torch.int64, p.B),
+        n, rp, _need(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+
+
+def _pool_args(p, w_s, b_pos, gamma):
+    f32 = torch.float32
+    return (_need(w_s, "w_s", f32, p.d), _need(b_pos, "b_pos", f32, p.m + p.overlap),
+            _need(gamma, "gamma", f32, p.d))
+
+
+def _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L_cap, N_cap):
+    f32 = torch.float32
+    return (_need(idx_tok, "idx_tok", torch.bfloat16, p.B, L_cap, p.D_I),
+            _need(w_s_idx, "w_s_idx", f32, p.D_I),
+            _need(b_pos_idx, "b_pos_idx", f32, p.m + p.overlap),
+            _need(idx_key, "idx_key", torch.uint8, p.B, N_cap, p.D_I),
+            _need(idx_scale, "idx_scale", f32, p.B, N_cap))
+
+
+def hca_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv4,
+                       dev_status=None, stream=None):
+    """hca_compress into a 4-bit cache."""
+    _check(lib().hca_compress_mxfp4(
+        C.byref(p), _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d), kv_tok.shape[1],
+        _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
+        n_blocks, _need_cache(p, kv4), kv4.shape[1], _ptr(dev_status), _stream(stream)))
+
+
+def csa_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv4,
+                       idx_tok=None, w_s_idx=None, b_pos_idx=None, idx_key=None, idx_scale=None,
+                       dev_status=None, stream=None):
+    """csa_compress into a 4-bit cache (indexer keys as csa_compress)."""
+    L, N = kv_tok.shape[1], kv4.shape[1]
+    _check(lib().csa_compress_mxfp4(
+        C.byref(p), _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d), L,
+        _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
+        n_blocks, _need_cache(p, kv4), N,
+        *_index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L, N),
+        _ptr(dev_status), _stream(stream)))
+
+
+def _mqa_inputs(p, rows, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse):
+    """Checked pointers of the attention's tensors, `rows` queries."""
+    bf, f32 = torch.bfloat16, torch.float32
+    return dict(q=_need(q, "q", bf, rows, p.H, p.d), kv4=_need_cache(p, kv4),
+                kv_tok=_must(kv_tok, "kv_tok", bf, p.B, None, p.d),
+                sink=_need(sink, "sink", f32, p.H), gq=_need(gamma_q, "gamma_q", f32, p.d),
+                gkv=_need(gamma_kv, "gamma_kv", f32, p.d), out=_need(out, "out", bf, rows, p.H, p.d),
+                lse=_need(lse, "lse", f32, rows, p.H))
+
+
+def sparse_mqa_decode_mxfp4(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink, out, gamma_q=None,
+                            gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
+    """sparse_mqa_decode over a 4-bit cache."""
+    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    _check(lib().sparse_mqa_decode_mxfp4(
+        C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
+        _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
+        _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
+        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _ptr(dev_status), _stream(stream)))
+
+
+def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, gamma_kv=None,
+                           lse=None, ws=None, dev_status=None, stream=None):
+    """dense_mqa_decode over a 4-bit cache."""
+    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    _check(lib().dense_mqa_decode_mxfp4(
+        C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
+        a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
+        _ptr(dev_status), _stream(stream)))
+
+
+def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
+                            idx_key, idx_scale, q, q_idx, q_scale, w, sink, topk_idx, topk_cnt,
+                            out, gamma_q=None, gamma_kv=None, ws=None, dev_status=None,
+                            stream=None):
+    """csa_prefill_chunk on a 4-bit cache (B = 1)."""
+    a = _mqa_inputs(p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, None)
+    L, N = kv_tok.shape[1], kv4.shape[1]
+    it, wsi, bpi, ik, isc = _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L,
+                                             N)
+    _check(lib().csa_prefill_chunk_mxfp4(
+        C.byref(p), P, T, a["kv_tok"], it, L, *_pool_args(p, w_s, b_pos, gamma), wsi, bpi, a["kv4"],
+        ik, isc, N, a["q"], _need(q_idx, "q_idx", torch.uint8, T, p.H_I, p.D_I),
+        _need(q_scale, "q_scale", torch.float32, T, p.H_I), _need(w, "w", torch.float32, T, p.H_I),
+        a["sink"], a["gq"], a["gkv"], _need(topk_idx, "topk_idx", torch.int32, T, p.k),
+        _need(topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws), _ptr(dev_status),
+        _stream(stream)))
+
+
+def hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
+                            gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
+    """hca_prefill_chunk on a 4-bit cache (B = 1)."""
+    a = _mqa_inputs(p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    _check(lib().hca_prefill_chunk_mxfp4(
+        C.byref(p), P, T, a["kv_tok"], kv_tok.shape[1], *_pool_args(p, w_s, b_pos, gamma), a["kv4"],
+        kv4.shape[1], a["q"], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
+        _ptr(dev_status), _stream(stream)))
+
+
+def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
+                          idx_key, idx_scale, q, q_idx, q_scale, w, sink, topk_idx, topk_cnt, out,
+                          gamma_q=None, gamma_kv=None, lse=None, ws=None, dev_status=None,
+                          stream=None):
+    """csa_decode_step on a 4-bit cache."""
+    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    L, N = kv_tok.shape[1], kv4.shape[1]
+    it, wsi, bpi, ik, isc = _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L,
+                                             N)
+    _check(lib().csa_decode_step_mxfp4(
+        C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], it, L,
+        *_pool_args(p, w_s, b_pos, gamma), wsi, bpi, a["kv4"], ik, isc, N, a["q"],
+        _need(q_idx, "q_idx", torch.uint8, p.B, p.H_I, p.D_I),
+        _need(q_scale, "q_scale", torch.float32, p.B, p.H_I),
+        _need(w, "w", torch.float32, p.B, p.H_I), a["sink"], a["gq"], a["gkv"],
+        _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
+        _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(ws),
+        _ptr(dev_status), _stream(stream)))
+
+
+def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
+                          gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
+    """hca_decode_step on a 4-bit cache."""
+    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    _check(lib().hca_decode_step_mxfp4(
+        C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
+        *_pool_args(p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
+        a["gkv"], a["out"], a["lse"], *_ws(ws), _ptr(dev_status), _stream(stream)))
 
 
 # ------------------------------------------- context split over several devices --

@@ -35,6 +35,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
     if ((p) != nullptr && !aligned16(p))                                               \
       return fail(CSA_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, #p);      \
   } while (0)
+// The compressed cache: bf16 entries (kv_c) or, with mx, MXFP4 rows (kv4).
+#define REQ_CACHE(p, mx)                                                               \
+  do {                                                                                 \
+    const char* nm = (mx) ? "kv4" : "kv_c";                                            \
+    if ((p) == nullptr) return fail(CSA_ERR_INVALID_ARG, "%s: %s is null", fn, nm);    \
+    if (!aligned16(p)) return fail(CSA_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, nm); \
+  } while (0)
 // 4-byte alignment suffices for small fp32 parameter vectors.
 #define REQ_PTR4(p)                                                                    \
   do {                                                                                 \
@@ -46,6 +53,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
   do {                                                                                 \
     if ((p) != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) != 0)                  \
       return fail(CSA_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", fn, #p);       \
+  } while (0)
+
+#define OPT_PTR8(p)                                                                    \
+  do {                                                                                 \
+    if ((p) != nullptr && (reinterpret_cast<uintptr_t>(p) & 7u) != 0)                  \
+      return fail(CSA_ERR_INVALID_ARG, "%s: %s is not 8-byte aligned", fn, #p);       \
   } while (0)
 
 csa_status check_common(const char* fn, const csa_params* p) {
@@ -266,16 +279,16 @@ size_t csa_workspace_bytes(const csa_params* p, csa_op op, int Q, int64_t N_cap)
 static csa_status compress_common(const char* fn, const csa_params* p, const void* kv_tok,
                                   int64_t L_cap, const int64_t* ctx_len, int64_t ctx_len_value,
                                   const float* w_s, const float* b_pos, const float* gamma,
-                                  int64_t first_block, int64_t n_blocks, void* kv_c,
-                                  int64_t N_cap, const void* idx_tok, const float* w_s_idx,
+                                  int64_t first_block, int64_t n_blocks, void* kv_c, int64_t N_cap,
+                                  const void* idx_tok, const float* w_s_idx,
                                   const float* b_pos_idx, uint8_t* idx_key, float* idx_scale,
-                                  int32_t* dev_status, void* stream,
+                                  int32_t* dev_status, void* stream, int mx,
                                   const int64_t* pos_newest = nullptr, int pdl_head = 0,
                                   int* ctas = nullptr) {
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;
   REQ_PTR(kv_tok);
-  REQ_PTR(kv_c);
+  REQ_CACHE(kv_c, mx);
   REQ_PTR4(w_s);
   REQ_PTR4(b_pos);
   OPT_PTR4(gamma);
@@ -321,6 +334,7 @@ static csa_status compress_common(const char* fn, const csa_params* p, const voi
   c.n_blocks = n_blocks;
   c.pos_newest = pos_newest;
   c.kv_c = kv_c;
+  c.mx = mx;
   c.idx_key = idx_key;
   c.idx_scale = idx_scale;
   c.eps = p->eps;
@@ -334,17 +348,28 @@ static csa_status compress_common(const char* fn, const csa_params* p, const voi
   return CSA_OK;
 }
 
-csa_status hca_compress(const csa_params* p, const void* kv_tok, int64_t L_cap,
-                        const int64_t* ctx_len, const float* w_s, const float* b_pos,
-                        const float* gamma, int64_t first_block, int64_t n_blocks, void* kv_c,
-                        int64_t N_cap, int32_t* dev_status, void* stream) {
-  const char* fn = "hca_compress";
+// ctx_len is required here (the chunk calls know the length instead).
+static csa_status compress_entry(const char* fn, const csa_params* p, const void* kv_tok,
+                                 int64_t L_cap, const int64_t* ctx_len, const float* w_s,
+                                 const float* b_pos, const float* gamma, int64_t first_block,
+                                 int64_t n_blocks, void* kv_c, int64_t N_cap, const void* idx_tok,
+                                 const float* w_s_idx, const float* b_pos_idx, uint8_t* idx_key,
+                                 float* idx_scale, int32_t* dev_status, void* stream, int mx) {
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;
   REQ_PTR(ctx_len);
   return compress_common(fn, p, kv_tok, L_cap, ctx_len, 0, w_s, b_pos, gamma, first_block,
-                         n_blocks, kv_c, N_cap, nullptr, nullptr, nullptr, nullptr, nullptr,
-                         dev_status, stream);
+                         n_blocks, kv_c, N_cap, idx_tok, w_s_idx, b_pos_idx, idx_key,
+                         idx_scale, dev_status, stream, mx);
+}
+
+csa_status hca_compress(const csa_params* p, const void* kv_tok, int64_t L_cap,
+                        const int64_t* ctx_len, const float* w_s, const float* b_pos,
+                        const float* gamma, int64_t first_block, int64_t n_blocks, void* kv_c,
+                        int64_t N_cap, int32_t* dev_status, void* stream) {
+  return compress_entry("hca_compress", p, kv_tok, L_cap, ctx_len, w_s, b_pos, gamma, first_block,
+                        n_blocks, kv_c, N_cap, nullptr, nullptr, nullptr, nullptr, nullptr,
+                        dev_status, stream, 0);
 }
 
 csa_status csa_compress(const csa_params* p, const void* kv_tok, int64_t L_cap,
@@ -353,21 +378,36 @@ csa_status csa_compress(const csa_params* p, const void* kv_tok, int64_t L_cap,
                         int64_t N_cap, const void* idx_tok, const float* w_s_idx,
                         const float* b_pos_idx, uint8_t* idx_key, float* idx_scale,
                         int32_t* dev_status, void* stream) {
-  const char* fn = "csa_compress";
-  csa_status st = check_common(fn, p);
-  if (st != CSA_OK) return st;
-  REQ_PTR(ctx_len);
-  return compress_common(fn, p, kv_tok, L_cap, ctx_len, 0, w_s, b_pos, gamma, first_block,
-                         n_blocks, kv_c, N_cap, idx_tok, w_s_idx, b_pos_idx, idx_key,
-                         idx_scale, dev_status, stream);
+  return compress_entry("csa_compress", p, kv_tok, L_cap, ctx_len, w_s, b_pos, gamma, first_block,
+                        n_blocks, kv_c, N_cap, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale,
+                        dev_status, stream, 0);
 }
 
-static csa_status index_common(const char* fn, const csa_params* p, int Q,
-                               const uint8_t* q_idx, const float* q_scale, const float* w,
-                               const uint8_t* idx_key, const float* idx_scale, int64_t N_cap,
-                               const int64_t* pos_q, int64_t pos_base, float* scores,
-                               int32_t* dev_status, cudaStream_t stream, int chained,
-                               const int64_t* safe_pos = nullptr,
+csa_status hca_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,
+                              const int64_t* ctx_len, const float* w_s, const float* b_pos,
+                              const float* gamma, int64_t first_block, int64_t n_blocks, void* kv4,
+                              int64_t N_cap, int32_t* dev_status, void* stream) {
+  return compress_entry("hca_compress_mxfp4", p, kv_tok, L_cap, ctx_len, w_s, b_pos, gamma,
+                        first_block, n_blocks, kv4, N_cap, nullptr, nullptr, nullptr, nullptr,
+                        nullptr, dev_status, stream, 1);
+}
+
+csa_status csa_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,
+                              const int64_t* ctx_len, const float* w_s, const float* b_pos,
+                              const float* gamma, int64_t first_block, int64_t n_blocks, void* kv4,
+                              int64_t N_cap, const void* idx_tok, const float* w_s_idx,
+                              const float* b_pos_idx, uint8_t* idx_key, float* idx_scale,
+                              int32_t* dev_status, void* stream) {
+  return compress_entry("csa_compress_mxfp4", p, kv_tok, L_cap, ctx_len, w_s, b_pos, gamma,
+                        first_block, n_blocks, kv4, N_cap, idx_tok, w_s_idx, b_pos_idx, idx_key,
+                        idx_scale, dev_status, stream, 1);
+}
+
+static csa_status index_common(const char* fn, const csa_params* p, int Q, const uint8_t* q_idx,
+                               const float* q_scale, const float* w, const uint8_t* idx_key,
+                               const float* idx_scale, int64_t N_cap, const int64_t* pos_q,
+                               int64_t pos_base, float* scores, int32_t* dev_status,
+                               cudaStream_t stream, int chained, const int64_t* safe_pos = nullptr,
                                int64_t safe_fixed = INT64_MAX, uint32_t* hist = nullptr,
                                int reserve_slots = 0) {
   csa::IndexLaunch a{};
@@ -426,10 +466,10 @@ static csa_status topk_common(const char* fn, const csa_params* p, int Q, const 
 
 static csa_status index_topk_common(const char* fn, const csa_params* p, int Q,
                                     const uint8_t* q_idx, const float* q_scale, const float* w,
-                                    const uint8_t* idx_key, const float* idx_scale,
-                                    int64_t N_cap, const int64_t* pos_q, int64_t pos_base,
-                                    int32_t* topk_idx, int32_t* topk_cnt, float* scores,
-                                    int32_t* dev_status, cudaStream_t stream, int chained,
+                                    const uint8_t* idx_key, const float* idx_scale, int64_t N_cap,
+                                    const int64_t* pos_q, int64_t pos_base, int32_t* topk_idx,
+                                    int32_t* topk_cnt, float* scores, int32_t* dev_status,
+                                    cudaStream_t stream, int chained,
                                     const int64_t* safe_pos = nullptr,
                                     int64_t safe_fixed = INT64_MAX, uint32_t* hist = nullptr,
                                     int32_t* path = nullptr, int reserve_slots = 0) {
@@ -459,8 +499,8 @@ static csa_status check_index_args(const char* fn, const csa_params* p, int Q, i
 csa_status lightning_index_topk(const csa_params* p, int Q, const uint8_t* q_idx,
                                 const float* q_scale, const float* w, const uint8_t* idx_key,
                                 const float* idx_scale, int64_t N_cap, const int64_t* pos_q,
-                                int32_t* topk_idx, int32_t* topk_cnt, float* scores_out,
-                                void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+                                int32_t* topk_idx, int32_t* topk_cnt, float* scores_out, void* ws,
+                                size_t ws_bytes, int32_t* dev_status, void* stream) {
   const char* fn = "lightning_index_topk";
   csa_status st = check_index_args(fn, p, Q, N_cap);
   if (st != CSA_OK) return st;
@@ -527,8 +567,8 @@ static csa_status mqa_common(const char* fn, const csa_params* p, csa_op op, int
                              const void* kv_c, int64_t N_cap, const int32_t* sel_idx,
                              const int32_t* sel_cnt, const void* kv_tok, int64_t L_cap,
                              const float* sink, const float* gamma_q, const float* gamma_kv,
-                             void* out, float* lse, void* ws, size_t ws_bytes,
-                             int32_t* dev_status, cudaStream_t stream, int chained,
+                             void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                             cudaStream_t stream, int chained, int mx,
                              const int64_t* safe_pos = nullptr, int64_t safe_fixed = 0,
                              int reserve = 0) {
   int splits = splits_for(p, op, rows, N_cap, reserve);
@@ -551,6 +591,7 @@ static csa_status mqa_common(const char* fn, const csa_params* p, csa_op op, int
   a.pos_q = pos_q;
   a.pos_base = pos_base;
   a.kv_c = kv_c;
+  a.mx = mx;
   a.sel_idx = sel_idx;
   a.sel_cnt = sel_cnt;
   a.kmax = p->k;
@@ -581,14 +622,14 @@ static csa_status check_mqa_args(const char* fn, const csa_params* p, const void
                                  const int64_t* pos_q, const void* kv_c, int64_t N_cap,
                                  const void* kv_tok, int64_t L_cap, const float* sink,
                                  const float* gamma_q, const float* gamma_kv, void* out,
-                                 float* lse, int32_t* dev_status) {
+                                 float* lse, int32_t* dev_status, int mx) {
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;
   st = check_attention(fn, p);
   if (st != CSA_OK) return st;
   REQ_PTR(q);
   REQ_PTR(pos_q);
-  REQ_PTR(kv_c);
+  REQ_CACHE(kv_c, mx);
   REQ_PTR(kv_tok);
   REQ_PTR4(sink);
   OPT_PTR4(gamma_q);
@@ -604,15 +645,15 @@ static csa_status check_mqa_args(const char* fn, const csa_params* p, const void
   return CSA_OK;
 }
 
-csa_status sparse_mqa_decode(const csa_params* p, const void* q, const int64_t* pos_q,
-                             const void* kv_c, int64_t N_cap, const int32_t* topk_idx,
-                             const int32_t* topk_cnt, const void* kv_tok, int64_t L_cap,
-                             const float* sink, const float* gamma_q, const float* gamma_kv,
-                             void* out, float* lse, void* ws, size_t ws_bytes,
-                             int32_t* dev_status, void* stream) {
-  const char* fn = "sparse_mqa_decode";
+static csa_status sparse_decode(const char* fn, const csa_params* p, const void* q,
+                                const int64_t* pos_q, const void* kv_c, int64_t N_cap,
+                                const int32_t* topk_idx, const int32_t* topk_cnt,
+                                const void* kv_tok, int64_t L_cap, const float* sink,
+                                const float* gamma_q, const float* gamma_kv, void* out, float* lse,
+                                void* ws, size_t ws_bytes, int32_t* dev_status, void* stream,
+                                int mx) {
   csa_status st = check_mqa_args(fn, p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q,
-                                 gamma_kv, out, lse, dev_status);
+                                 gamma_kv, out, lse, dev_status, mx);
   if (st != CSA_OK) return st;
   if (p->k < 1 || p->k > kMaxTopk)
     return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: k=%d (supported: 1..%d)", fn, p->k, kMaxTopk);
@@ -620,33 +661,72 @@ csa_status sparse_mqa_decode(const csa_params* p, const void* q, const int64_t* 
   REQ_PTR4(topk_cnt);
   return mqa_common(fn, p, CSA_OP_SPARSE_MQA, p->B, 1, q, pos_q, 0, kv_c, N_cap, topk_idx,
                     topk_cnt, kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes,
-                    dev_status, static_cast<cudaStream_t>(stream), 0);
+                    dev_status, static_cast<cudaStream_t>(stream), 0, mx);
+}
+
+csa_status sparse_mqa_decode(const csa_params* p, const void* q, const int64_t* pos_q,
+                             const void* kv_c, int64_t N_cap, const int32_t* topk_idx,
+                             const int32_t* topk_cnt, const void* kv_tok, int64_t L_cap,
+                             const float* sink, const float* gamma_q, const float* gamma_kv,
+                             void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                             void* stream) {
+  return sparse_decode("sparse_mqa_decode", p, q, pos_q, kv_c, N_cap, topk_idx, topk_cnt, kv_tok,
+                       L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream,
+                       0);
+}
+
+csa_status sparse_mqa_decode_mxfp4(const csa_params* p, const void* q, const int64_t* pos_q,
+                                   const void* kv4, int64_t N_cap, const int32_t* topk_idx,
+                                   const int32_t* topk_cnt, const void* kv_tok, int64_t L_cap,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   void* out, float* lse, void* ws, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream) {
+  return sparse_decode("sparse_mqa_decode_mxfp4", p, q, pos_q, kv4, N_cap, topk_idx, topk_cnt,
+                       kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status,
+                       stream, 1);
+}
+
+static csa_status dense_decode(const char* fn, const csa_params* p, const void* q,
+                               const int64_t* pos_q, const void* kv_c, int64_t N_cap,
+                               const void* kv_tok, int64_t L_cap, const float* sink,
+                               const float* gamma_q, const float* gamma_kv, void* out, float* lse,
+                               void* ws, size_t ws_bytes, int32_t* dev_status, void* stream,
+                               int mx) {
+  csa_status st = check_mqa_args(fn, p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q,
+                                 gamma_kv, out, lse, dev_status, mx);
+  if (st != CSA_OK) return st;
+  return mqa_common(fn, p, CSA_OP_DENSE_MQA, p->B, 1, q, pos_q, 0, kv_c, N_cap, nullptr,
+                    nullptr, kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes,
+                    dev_status, static_cast<cudaStream_t>(stream), 0, mx);
 }
 
 csa_status dense_mqa_decode(const csa_params* p, const void* q, const int64_t* pos_q,
                             const void* kv_c, int64_t N_cap, const void* kv_tok, int64_t L_cap,
                             const float* sink, const float* gamma_q, const float* gamma_kv,
-                            void* out, float* lse, void* ws, size_t ws_bytes,
-                            int32_t* dev_status, void* stream) {
-  const char* fn = "dense_mqa_decode";
-  csa_status st = check_mqa_args(fn, p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q,
-                                 gamma_kv, out, lse, dev_status);
-  if (st != CSA_OK) return st;
-  return mqa_common(fn, p, CSA_OP_DENSE_MQA, p->B, 1, q, pos_q, 0, kv_c, N_cap, nullptr,
-                    nullptr, kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes,
-                    dev_status, static_cast<cudaStream_t>(stream), 0);
+                            void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                            void* stream) {
+  return dense_decode("dense_mqa_decode", p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q,
+                      gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 0);
 }
 
-csa_status csa_prefill_chunk(const csa_params* p, int64_t P, int T, const void* kv_tok,
-                             const void* idx_tok, int64_t L_cap, const float* w_s,
-                             const float* b_pos, const float* gamma, const float* w_s_idx,
-                             const float* b_pos_idx, void* kv_c, uint8_t* idx_key,
-                             float* idx_scale, int64_t N_cap, const void* q,
-                             const uint8_t* q_idx, const float* q_scale, const float* w,
-                             const float* sink, const float* gamma_q, const float* gamma_kv,
-                             int32_t* topk_idx, int32_t* topk_cnt, void* out, void* ws,
-                             size_t ws_bytes, int32_t* dev_status, void* stream) {
-  const char* fn = "csa_prefill_chunk";
+csa_status dense_mqa_decode_mxfp4(const csa_params* p, const void* q, const int64_t* pos_q,
+                                  const void* kv4, int64_t N_cap, const void* kv_tok,
+                                  int64_t L_cap, const float* sink, const float* gamma_q,
+                                  const float* gamma_kv, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return dense_decode("dense_mqa_decode_mxfp4", p, q, pos_q, kv4, N_cap, kv_tok, L_cap, sink,
+                      gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 1);
+}
+
+static csa_status csa_chunk(const char* fn, const csa_params* p, int64_t P, int T,
+                            const void* kv_tok, const void* idx_tok, int64_t L_cap,
+                            const float* w_s, const float* b_pos, const float* gamma,
+                            const float* w_s_idx, const float* b_pos_idx, void* kv_c,
+                            uint8_t* idx_key, float* idx_scale, int64_t N_cap, const void* q,
+                            const uint8_t* q_idx, const float* q_scale, const float* w,
+                            const float* sink, const float* gamma_q, const float* gamma_kv,
+                            int32_t* topk_idx, int32_t* topk_cnt, void* out, void* ws,
+                            size_t ws_bytes, int32_t* dev_status, void* stream, int mx) {
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;
   if (p->B != 1) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: B=%d (supported: 1)", fn, p->B);
@@ -675,7 +755,7 @@ csa_status csa_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
   REQ_PTR(topk_idx);
   REQ_PTR4(topk_cnt);
   REQ_PTR(out);
-  REQ_PTR(kv_c);
+  REQ_CACHE(kv_c, mx);
   REQ_PTR(kv_tok);
   size_t need = csa_workspace_bytes(p, CSA_OP_PREFILL, T, N_cap);
   if (!ws || ws_bytes < need)
@@ -687,7 +767,7 @@ csa_status csa_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
   int64_t b0 = P / p->m;
   st = compress_common(fn, p, kv_tok, L_cap, nullptr, P + T, w_s, b_pos, gamma, b0,
                        nblk_total - b0, kv_c, N_cap, idx_tok, w_s_idx, b_pos_idx, idx_key,
-                       idx_scale, dev_status, stream);
+                       idx_scale, dev_status, stream, mx);
   if (st != CSA_OK) return st;
   // 2-3. Causal indexer and top-k for the T queries at positions P .. P+T-1.
   float* scores = static_cast<float*>(ws);
@@ -701,23 +781,50 @@ csa_status csa_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
   size_t rest_bytes = ws_bytes - scores_bytes(T, N_cap);
   return mqa_common(fn, p, CSA_OP_SPARSE_MQA, T, T, q, nullptr, P, kv_c, N_cap, topk_idx,
                     topk_cnt, kv_tok, L_cap, sink, gamma_q, gamma_kv, out, nullptr, rest,
-                    rest_bytes, dev_status, s, 1);
+                    rest_bytes, dev_status, s, 1, mx);
 }
 
-csa_status csa_decode_step(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
-                           const void* idx_tok, int64_t L_cap, const float* w_s,
-                           const float* b_pos, const float* gamma, const float* w_s_idx,
-                           const float* b_pos_idx, void* kv_c, uint8_t* idx_key,
-                           float* idx_scale, int64_t N_cap, const void* q, const uint8_t* q_idx,
-                           const float* q_scale, const float* w, const float* sink,
-                           const float* gamma_q, const float* gamma_kv, int32_t* topk_idx,
-                           int32_t* topk_cnt, void* out, float* lse, void* ws, size_t ws_bytes,
-                           int32_t* dev_status, void* stream) {
-  const char* fn = "csa_decode_step";
+csa_status csa_prefill_chunk(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                             const void* idx_tok, int64_t L_cap, const float* w_s,
+                             const float* b_pos, const float* gamma, const float* w_s_idx,
+                             const float* b_pos_idx, void* kv_c, uint8_t* idx_key,
+                             float* idx_scale, int64_t N_cap, const void* q, const uint8_t* q_idx,
+                             const float* q_scale, const float* w, const float* sink,
+                             const float* gamma_q, const float* gamma_kv, int32_t* topk_idx,
+                             int32_t* topk_cnt, void* out, void* ws, size_t ws_bytes,
+                             int32_t* dev_status, void* stream) {
+  return csa_chunk("csa_prefill_chunk", p, P, T, kv_tok, idx_tok, L_cap, w_s, b_pos, gamma,
+                   w_s_idx, b_pos_idx, kv_c, idx_key, idx_scale, N_cap, q, q_idx, q_scale, w, sink,
+                   gamma_q, gamma_kv, topk_idx, topk_cnt, out, ws, ws_bytes, dev_status, stream, 0);
+}
+
+csa_status csa_prefill_chunk_mxfp4(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                                   const void* idx_tok, int64_t L_cap, const float* w_s,
+                                   const float* b_pos, const float* gamma, const float* w_s_idx,
+                                   const float* b_pos_idx, void* kv4, uint8_t* idx_key,
+                                   float* idx_scale, int64_t N_cap, const void* q,
+                                   const uint8_t* q_idx, const float* q_scale, const float* w,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   int32_t* topk_idx, int32_t* topk_cnt, void* out, void* ws,
+                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return csa_chunk("csa_prefill_chunk_mxfp4", p, P, T, kv_tok, idx_tok, L_cap, w_s, b_pos, gamma,
+                   w_s_idx, b_pos_idx, kv4, idx_key, idx_scale, N_cap, q, q_idx, q_scale, w, sink,
+                   gamma_q, gamma_kv, topk_idx, topk_cnt, out, ws, ws_bytes, dev_status, stream, 1);
+}
+
+static csa_status csa_step(const char* fn, const csa_params* p, const int64_t* pos_q,
+                           const void* kv_tok, const void* idx_tok, int64_t L_cap,
+                           const float* w_s, const float* b_pos, const float* gamma,
+                           const float* w_s_idx, const float* b_pos_idx, void* kv_c,
+                           uint8_t* idx_key, float* idx_scale, int64_t N_cap, const void* q,
+                           const uint8_t* q_idx, const float* q_scale, const float* w,
+                           const float* sink, const float* gamma_q, const float* gamma_kv,
+                           int32_t* topk_idx, int32_t* topk_cnt, void* out, float* lse, void* ws,
+                           size_t ws_bytes, int32_t* dev_status, void* stream, int mx) {
   csa_status st = check_index_args(fn, p, 1, N_cap);
   if (st != CSA_OK) return st;
   st = check_mqa_args(fn, p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q, gamma_kv, out,
-                      lse, dev_status);
+                      lse, dev_status, mx);
   if (st != CSA_OK) return st;
   if (p->k < 1 || p->k > kMaxTopk)
     return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: k=%d (supported: 1..%d)", fn, p->k, kMaxTopk);
@@ -737,8 +844,8 @@ csa_status csa_decode_step(const csa_params* p, const int64_t* pos_q, const void
   // pooled over the tokens up to it.
   int compress_ctas = 0;
   st = compress_common(fn, p, kv_tok, L_cap, nullptr, 0, w_s, b_pos, gamma, 0, 1, kv_c, N_cap,
-                       idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, dev_status, stream, pos_q,
-                       1, &compress_ctas);
+                       idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, dev_status, stream, mx,
+                       pos_q, 1, &compress_ctas);
   if (st != CSA_OK) return st;
   // 2-3. Indexer and top-k over each sequence's visible entries (the indexer
   // grid leaves out the slots the compression CTAs hold).  Where the
@@ -759,19 +866,47 @@ csa_status csa_decode_step(const csa_params* p, const int64_t* pos_q, const void
   char* rest = static_cast<char*>(ws) + head;
   return mqa_common(fn, p, CSA_OP_SPARSE_MQA, p->B, 1, q, pos_q, 0, kv_c, N_cap, topk_idx,
                     topk_cnt, kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, rest,
-                    ws_bytes - head, dev_status, s, 1, nullptr, 0,
+                    ws_bytes - head, dev_status, s, 1, mx, nullptr, 0,
                     decode_step_reserve(p, N_cap));
 }
 
-csa_status hca_decode_step(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
-                           int64_t L_cap, const float* w_s, const float* b_pos,
+csa_status csa_decode_step(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                           const void* idx_tok, int64_t L_cap, const float* w_s,
+                           const float* b_pos, const float* gamma, const float* w_s_idx,
+                           const float* b_pos_idx, void* kv_c, uint8_t* idx_key, float* idx_scale,
+                           int64_t N_cap, const void* q, const uint8_t* q_idx,
+                           const float* q_scale, const float* w, const float* sink,
+                           const float* gamma_q, const float* gamma_kv, int32_t* topk_idx,
+                           int32_t* topk_cnt, void* out, float* lse, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+  return csa_step("csa_decode_step", p, pos_q, kv_tok, idx_tok, L_cap, w_s, b_pos, gamma, w_s_idx,
+                  b_pos_idx, kv_c, idx_key, idx_scale, N_cap, q, q_idx, q_scale, w, sink, gamma_q,
+                  gamma_kv, topk_idx, topk_cnt, out, lse, ws, ws_bytes, dev_status, stream, 0);
+}
+
+csa_status csa_decode_step_mxfp4(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                                 const void* idx_tok, int64_t L_cap, const float* w_s,
+                                 const float* b_pos, const float* gamma, const float* w_s_idx,
+                                 const float* b_pos_idx, void* kv4, uint8_t* idx_key,
+                                 float* idx_scale, int64_t N_cap, const void* q,
+                                 const uint8_t* q_idx, const float* q_scale, const float* w,
+                                 const float* sink, const float* gamma_q, const float* gamma_kv,
+                                 int32_t* topk_idx, int32_t* topk_cnt, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return csa_step("csa_decode_step_mxfp4", p, pos_q, kv_tok, idx_tok, L_cap, w_s, b_pos, gamma,
+                  w_s_idx, b_pos_idx, kv4, idx_key, idx_scale, N_cap, q, q_idx, q_scale, w, sink,
+                  gamma_q, gamma_kv, topk_idx, topk_cnt, out, lse, ws, ws_bytes, dev_status,
+                  stream, 1);
+}
+
+static csa_status hca_step(const char* fn, const csa_params* p, const int64_t* pos_q,
+                           const void* kv_tok, int64_t L_cap, const float* w_s, const float* b_pos,
                            const float* gamma, void* kv_c, int64_t N_cap, const void* q,
                            const float* sink, const float* gamma_q, const float* gamma_kv,
-                           void* out, float* lse, void* ws, size_t ws_bytes,
-                           int32_t* dev_status, void* stream) {
-  const char* fn = "hca_decode_step";
+                           void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                           void* stream, int mx) {
   csa_status st = check_mqa_args(fn, p, q, pos_q, kv_c, N_cap, kv_tok, L_cap, sink, gamma_q,
-                                 gamma_kv, out, lse, dev_status);
+                                 gamma_kv, out, lse, dev_status, mx);
   if (st != CSA_OK) return st;
   size_t need = csa_workspace_bytes(p, CSA_OP_HCA_DECODE_STEP, 1, N_cap);
   if (!ws || ws_bytes < need)
@@ -780,22 +915,40 @@ csa_status hca_decode_step(const csa_params* p, const int64_t* pos_q, const void
   if (!aligned16(ws)) return fail(CSA_ERR_INVALID_ARG, "%s: ws is not 16-byte aligned", fn);
   // 1. Each sequence's newest block, then 2. dense MQA with window and sink.
   st = compress_common(fn, p, kv_tok, L_cap, nullptr, 0, w_s, b_pos, gamma, 0, 1, kv_c, N_cap,
-                       nullptr, nullptr, nullptr, nullptr, nullptr, dev_status, stream, pos_q, 1);
+                       nullptr, nullptr, nullptr, nullptr, nullptr, dev_status, stream, mx, pos_q, 1);
   if (st != CSA_OK) return st;
   // Only each sequence's newest block is written by this call: the older
   // entries stream in while it is compressed.
   return mqa_common(fn, p, CSA_OP_DENSE_MQA, p->B, 1, q, pos_q, 0, kv_c, N_cap, nullptr, nullptr,
                     kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status,
-                    static_cast<cudaStream_t>(stream), 1, pos_q, 0, p->B);
+                    static_cast<cudaStream_t>(stream), 1, mx, pos_q, 0, p->B);
 }
 
-csa_status hca_prefill_chunk(const csa_params* p, int64_t P, int T, const void* kv_tok,
-                             int64_t L_cap, const float* w_s, const float* b_pos,
-                             const float* gamma, void* kv_c, int64_t N_cap, const void* q,
-                             const float* sink, const float* gamma_q, const float* gamma_kv,
-                             void* out, float* lse, void* ws, size_t ws_bytes,
-                             int32_t* dev_status, void* stream) {
-  const char* fn = "hca_prefill_chunk";
+csa_status hca_decode_step(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                           int64_t L_cap, const float* w_s, const float* b_pos, const float* gamma,
+                           void* kv_c, int64_t N_cap, const void* q, const float* sink,
+                           const float* gamma_q, const float* gamma_kv, void* out, float* lse,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return hca_step("hca_decode_step", p, pos_q, kv_tok, L_cap, w_s, b_pos, gamma, kv_c, N_cap, q,
+                  sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 0);
+}
+
+csa_status hca_decode_step_mxfp4(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                                 int64_t L_cap, const float* w_s, const float* b_pos,
+                                 const float* gamma, void* kv4, int64_t N_cap, const void* q,
+                                 const float* sink, const float* gamma_q, const float* gamma_kv,
+                                 void* out, float* lse, void* ws, size_t ws_bytes,
+                                 int32_t* dev_status, void* stream) {
+  return hca_step("hca_decode_step_mxfp4", p, pos_q, kv_tok, L_cap, w_s, b_pos, gamma, kv4, N_cap,
+                  q, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 1);
+}
+
+static csa_status hca_chunk(const char* fn, const csa_params* p, int64_t P, int T,
+                            const void* kv_tok, int64_t L_cap, const float* w_s,
+                            const float* b_pos, const float* gamma, void* kv_c, int64_t N_cap,
+                            const void* q, const float* sink, const float* gamma_q,
+                            const float* gamma_kv, void* out, float* lse, void* ws,
+                            size_t ws_bytes, int32_t* dev_status, void* stream, int mx) {
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;
   if (p->B != 1) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: B=%d (supported: 1)", fn, p->B);
@@ -832,13 +985,115 @@ csa_status hca_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
   const int64_t b0 = P / p->m;
   st = compress_common(fn, p, kv_tok, L_cap, nullptr, P + T, w_s, b_pos, gamma, b0,
                        nblk_total - b0, kv_c, N_cap, nullptr, nullptr, nullptr, nullptr, nullptr,
-                       dev_status, stream);
+                       dev_status, stream, mx);
   if (st != CSA_OK) return st;
   // 2. Dense MQA per query over its visible entries and its causal window
   // (entries below b0 were written before the call).
   return mqa_common(fn, p, CSA_OP_DENSE_MQA, T, T, q, nullptr, P, kv_c, N_cap, nullptr, nullptr,
                     kv_tok, L_cap, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status,
-                    static_cast<cudaStream_t>(stream), 1, nullptr, b0);
+                    static_cast<cudaStream_t>(stream), 1, mx, nullptr, b0);
+}
+
+csa_status hca_prefill_chunk(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                             int64_t L_cap, const float* w_s, const float* b_pos,
+                             const float* gamma, void* kv_c, int64_t N_cap, const void* q,
+                             const float* sink, const float* gamma_q, const float* gamma_kv,
+                             void* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                             void* stream) {
+  return hca_chunk("hca_prefill_chunk", p, P, T, kv_tok, L_cap, w_s, b_pos, gamma, kv_c, N_cap, q,
+                   sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 0);
+}
+
+csa_status hca_prefill_chunk_mxfp4(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                                   int64_t L_cap, const float* w_s, const float* b_pos,
+                                   const float* gamma, void* kv4, int64_t N_cap, const void* q,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   void* out, float* lse, void* ws, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream) {
+  return hca_chunk("hca_prefill_chunk_mxfp4", p, P, T, kv_tok, L_cap, w_s, b_pos, gamma, kv4,
+                   N_cap, q, sink, gamma_q, gamma_kv, out, lse, ws, ws_bytes, dev_status, stream, 1);
+}
+
+// ------------------------------------------------------------- MXFP4 cache --
+size_t mxfp4_row_bytes(int d) {
+  if (d != 128 && d != 512) {
+    fail(CSA_ERR_UNSUPPORTED_SHAPE, "mxfp4_row_bytes: d=%d (supported: 128, 512)", d);
+    return 0;
+  }
+  return (size_t)csa::mx_row_bytes(d);
+}
+
+static csa_status check_cache(const char* fn, const csa_params* p, int64_t n, int64_t N_cap) {
+  csa_status st = check_common(fn, p);
+  if (st != CSA_OK) return st;
+  if (p->B > 65535) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: B=%d (supported: <= 65535)", fn, p->B);
+  if (n < 0 || N_cap < 1 || N_cap > ((int64_t)1 << 31) - 1 || n > ((int64_t)1 << 31) - 1)
+    return fail(CSA_ERR_INVALID_ARG, "%s: n=%lld N_cap=%lld", fn, (long long)n, (long long)N_cap);
+  return CSA_OK;
+}
+
+csa_status mxfp4_cache_write(const csa_params* p, const void* rows, int64_t seq_stride, int64_t n,
+                             const int64_t* first_entry, const int64_t* count, void* kv4,
+                             int64_t N_cap, int32_t* dev_status, void* stream) {
+  const char* fn = "mxfp4_cache_write";
+  csa_status st = check_cache(fn, p, n, N_cap);
+  if (st != CSA_OK) return st;
+  if (n == 0) return CSA_OK;
+  REQ_PTR(rows);
+  if (seq_stride < 0 || seq_stride % 8 || (p->B > 1 && seq_stride < n * p->d) ||
+      seq_stride > ((int64_t)1 << 46))
+    return fail(CSA_ERR_INVALID_ARG,
+                "%s: seq_stride=%lld must be a multiple of 8 and at least n*d", fn,
+                (long long)seq_stride);
+  OPT_PTR8(first_entry);
+  OPT_PTR8(count);
+  REQ_PTR(kv4);
+  OPT_PTR4(dev_status);
+  csa::MxCacheLaunch c{};
+  c.B = p->B;
+  c.d = p->d;
+  c.n = n;
+  c.n_cap = N_cap;
+  c.rows_in = rows;
+  c.seq_bytes = seq_stride * 2;
+  c.first = first_entry;
+  c.count = count;
+  c.cache = kv4;
+  c.status = dev_status;
+  cudaError_t e = csa::launch_mx_cache_write(c, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return CSA_OK;
+}
+
+csa_status mxfp4_cache_read(const csa_params* p, const void* kv4, int64_t N_cap,
+                            const int32_t* idx, const int64_t* first_entry, const int64_t* count,
+                            int64_t n, void* rows, int32_t* dev_status, void* stream) {
+  const char* fn = "mxfp4_cache_read";
+  csa_status st = check_cache(fn, p, n, N_cap);
+  if (st != CSA_OK) return st;
+  if (n == 0) return CSA_OK;
+  REQ_PTR(kv4);
+  OPT_PTR4(idx);
+  OPT_PTR8(first_entry);
+  OPT_PTR8(count);
+  if (idx && first_entry)
+    return fail(CSA_ERR_INVALID_ARG, "%s: idx and first_entry exclude each other", fn);
+  REQ_PTR(rows);
+  OPT_PTR4(dev_status);
+  csa::MxCacheLaunch c{};
+  c.B = p->B;
+  c.d = p->d;
+  c.n = n;
+  c.n_cap = N_cap;
+  c.rows_out = rows;
+  c.idx = idx;
+  c.first = first_entry;
+  c.count = count;
+  c.cache = const_cast<void*>(kv4);
+  c.status = dev_status;
+  cudaError_t e = csa::launch_mx_cache_read(c, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return CSA_OK;
 }
 
 // ------------------------------------------------- grouped output projection --
@@ -1006,11 +1261,12 @@ csa_status csa_merge_candidates(const csa_params* p, int Q, int G, const float* 
   return CSA_OK;
 }
 
-csa_status sparse_mqa_partials(const csa_params* p, int splits, const void* q, const int64_t* pos_q,
-                               const void* kv_c, int64_t N_cap, const int32_t* topk_idx,
-                               const int32_t* topk_cnt, const void* kv_tok, int64_t L_cap,
-                               const float* gamma_q, const float* gamma_kv, void* part_o,
-                               float* part_ml, int32_t* dev_status, void* stream) {
+csa_status sparse_mqa_partials(const csa_params* p, int splits, const void* q,
+                               const int64_t* pos_q, const void* kv_c, int64_t N_cap,
+                               const int32_t* topk_idx, const int32_t* topk_cnt,
+                               const void* kv_tok, int64_t L_cap, const float* gamma_q,
+                               const float* gamma_kv, void* part_o, float* part_ml,
+                               int32_t* dev_status, void* stream) {
   const char* fn = "sparse_mqa_partials";
   csa_status st = check_common(fn, p);
   if (st != CSA_OK) return st;

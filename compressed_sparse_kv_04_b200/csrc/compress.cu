@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mxfp4.cuh"
 
 namespace csa {
 namespace {
@@ -45,6 +46,7 @@ struct StreamArgs {
   float* out_scale;          // [B, N_cap] (with out_e4m3)
   int dim;
   int rope_dim;              // > 0: the entry is stored rotated to (i+1)*m - 1
+  uint8_t* out_mx;           // [B, N_cap, mx_row_bytes(dim)] or null
 };
 
 struct PoolArgs {
@@ -236,6 +238,31 @@ CSA_DEV void finish_row(const StreamArgs& sa, const PoolArgs& a, int64_t row, in
         *reinterpret_cast<uint32_t*>(d) = w[0];
     }
   }
+  if constexpr (DIM >= 128) {
+    if (sa.out_mx) {
+      // The row as the bf16 cache would hold it, then MXFP4: the same bytes
+      // as quantising the stored bf16 row.
+      constexpr int BL = kMxBlock / LN::VEC;  // lanes per block
+      uint8_t* dst = sa.out_mx + row * mx_row_bytes(DIM);
+#pragma unroll
+      for (int part = 0; part < LN::NPART; ++part) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int q = 0; q < LN::VEC / 2; ++q)
+          w[q] = pack_bf16(p[part * LN::VEC + 2 * q], p[part * LN::VEC + 2 * q + 1]);
+        uint32_t am = mx_amax8(w);
+#pragma unroll
+        for (int o = 1; o < BL; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        const uint32_t s = mx_scale_byte(am), codes = mx_quantise8(w, s);
+        const int e0 = LN::elem(lane, part, 0);
+        if constexpr (LN::VEC == 8)
+          *reinterpret_cast<uint32_t*>(dst + e0 / 2) = codes;
+        else
+          *reinterpret_cast<uint16_t*>(dst + e0 / 2) = (uint16_t)codes;
+        if (lane % BL == 0) dst[DIM / 2 + e0 / kMxBlock] = (uint8_t)s;
+      }
+    }
+  }
   if (sa.out_e4m3) {
     float amax = 0.f;
 #pragma unroll
@@ -414,10 +441,11 @@ cudaError_t launch_compress(const CompressLaunch& c, cudaStream_t stream) {
   PoolArgs a{};
   a.nstreams = c.idx_tok ? 2 : 1;
   a.s[0] = StreamArgs{reinterpret_cast<const __nv_bfloat16*>(c.kv_tok), c.w_s, c.b_pos, c.gamma,
-                      reinterpret_cast<__nv_bfloat16*>(c.kv_c), nullptr, nullptr, c.d, c.rope_dim};
+                      c.mx ? nullptr : reinterpret_cast<__nv_bfloat16*>(c.kv_c), nullptr, nullptr,
+                      c.d, c.rope_dim, c.mx ? static_cast<uint8_t*>(c.kv_c) : nullptr};
   if (c.idx_tok)
     a.s[1] = StreamArgs{reinterpret_cast<const __nv_bfloat16*>(c.idx_tok), c.w_s_idx, c.b_pos_idx,
-                        nullptr, nullptr, c.idx_key, c.idx_scale, c.D_I, 0};
+                        nullptr, nullptr, c.idx_key, c.idx_scale, c.D_I, 0, nullptr};
   for (int j = 0; j < 64; ++j) a.inv_freq[j] = c.inv_freq[j];
   a.B = c.B;
   a.m = c.m;

@@ -26,7 +26,8 @@ struct CompressLaunch {
   const float *w_s, *b_pos, *gamma, *w_s_idx, *b_pos_idx;
   int64_t first_block, n_blocks;
   const int64_t* pos_newest;  // [B] or null: one block per sequence, the one holding pos
-  void* kv_c;
+  void* kv_c;               // bf16 entries, or with mx != 0 MXFP4 cache rows
+  int mx;
   uint8_t* idx_key;
   float* idx_scale;
   float eps;
@@ -136,7 +137,8 @@ struct MqaLaunch {
   const void* q;            // [B*Q, H, D] bf16
   const int64_t* pos_q;     // [B*Q] or null -> pos_base + (row % Q)
   int64_t pos_base;
-  const void* kv_c;         // [B, N_cap, D]
+  const void* kv_c;         // [B, N_cap, D] bf16, or with mx != 0 MXFP4 rows
+  int mx;
   const int32_t* sel_idx;   // [B*Q, kmax] or null (dense)
   const int32_t* sel_cnt;   // [B*Q]
   int kmax;
@@ -188,6 +190,28 @@ struct ProjGemm {
 cudaError_t launch_proj_gemm(const ProjGemm& g, cudaStream_t stream);
 int proj_token_tile(int T);
 int proj_choose_splits(int T, int N, int groups, int K, int num_sms);
+
+// Bytes of an MXFP4 cache row of d values: codes, then scale bytes, padded so
+// that every row starts on a 16-byte boundary.
+__host__ __device__ constexpr int mx_row_bytes(int d) { return (d / 2 + d / 32 + 15) / 16 * 16; }
+
+// Rows written into an MXFP4 cache, or read back from it: per sequence b the
+// rows i < count[b] (n without counts) are entries first[b] + i (or, reading,
+// idx[b, i]; -1 is skipped).
+struct MxCacheLaunch {
+  int B, d;
+  int64_t n, n_cap;
+  const void* rows_in;      // write: [B] x [n, d] bf16, seq_bytes apart
+  int64_t seq_bytes;
+  void* rows_out;           // read: [B, n, d] bf16
+  const int32_t* idx;       // read: [B, n] or null
+  const int64_t* first;     // [B] or null (0)
+  const int64_t* count;     // [B] or null (n)
+  void* cache;              // [B, n_cap, row bytes]
+  int32_t* status;
+};
+cudaError_t launch_mx_cache_write(const MxCacheLaunch& c, cudaStream_t stream);
+cudaError_t launch_mx_cache_read(const MxCacheLaunch& c, cudaStream_t stream);
 
 int device_sm_count();
 
@@ -243,7 +267,8 @@ csa_status set_error(csa_status s, const char* fmt, ...);
 // Sets the dynamic shared-memory limit of `func` once per device (the call
 // is then skipped, which keeps launches legal inside CUDA-graph capture).
 // `slot` (0..31) identifies the kernel: each kernel instance has its own
-// (indexer 0-1, 15-16 and 19-20, top-k 2, 8-9 and 17, attention 3-7, projection 10-14).
+// (indexer 0-1, 15-16 and 19-20, top-k 2, 8-9 and 17, attention 3-7 and (over
+// an MXFP4 cache) 21-25, projection 10-14).
 cudaError_t ensure_smem_attr(const void* func, int slot, size_t bytes);
 
 }  // namespace csa

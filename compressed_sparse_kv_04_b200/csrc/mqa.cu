@@ -46,6 +46,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mxfp4.cuh"
 #include "tma.h"
 
 namespace csa {
@@ -112,6 +113,7 @@ struct Params {
   const int32_t* sel_cnt;
   int kmax;
   const __nv_bfloat16* kv_c;
+  const uint8_t* kv4;  // MXFP4 cache rows [B, N_cap, mx_row_bytes(D)] (kMx kernels)
   const float* gamma_q;
   const float* gamma_kv;
   float eps, scale_log2;  // softmax scale * log2(e)
@@ -137,6 +139,45 @@ struct Params {
 CSA_DEV uint32_t tile_off(int r, int d) {
   uint32_t lin = (uint32_t)r * 128u + (uint32_t)(d & 63) * 2u;
   return (uint32_t)(d >> 6) * (TN * 128u) + (lin ^ (((lin >> 7) & 7u) << 4));
+}
+
+// The 128 transform threads' blocks of an MXFP4 tile, as bf16 into the stage.
+// Thread tid holds block tid % (D/32) of rows tid / (D/32) + u * 4096/D: the
+// 16-byte units 4*(blk&1) .. +3 of the row's chunk blk/2.  The lanes of a row
+// write their units in rotated order, so that eight lanes fill eight
+// different units of the swizzled rows (no bank conflict).
+template <int D, bool kWide>
+CSA_DEV void mx_store_tile(uint8_t* st, int tid, const uint4 (&cd)[TN * D / 4096],
+                           const uint32_t (&sc)[TN * D / 4096]) {
+  constexpr int kBlk = D / kMxBlock;
+  const int blk = tid % kBlk, rot = (blk >> 1) & 3;
+#pragma unroll
+  for (int u = 0; u < TN * kBlk / 128; ++u) {
+    const int rr = u * (128 / kBlk) + tid / kBlk;
+    uint32_t w[4] = {cd[u].x, cd[u].y, cd[u].z, cd[u].w};
+    if (rot & 1) {
+      const uint32_t w0 = w[0];
+      w[0] = w[1];
+      w[1] = w[2];
+      w[2] = w[3];
+      w[3] = w0;
+    }
+    if (rot & 2) {
+      const uint32_t w0 = w[0], w1 = w[1];
+      w[0] = w[2];
+      w[1] = w[3];
+      w[2] = w0;
+      w[3] = w1;
+    }
+    const MxScale scale(sc[u]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o[4];
+      mx_values8<kWide>(w[j], scale, o);
+      *reinterpret_cast<uint4*>(st + tile_off(rr, kMxBlock * blk + 8 * ((j + rot) & 3))) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 CSA_DEV uint64_t desc_k(uint32_t saddr) { return sdesc_sw128(saddr, 16, 1024); }
@@ -288,7 +329,7 @@ __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int ro
   merge_head<D, R, G, true>(p, (int)(gw / p.H), (int)(gw % p.H), lane, wsm + warp * p.splits);
 }
 
-template <int D, int R>
+template <int D, int R, bool kMx>
 __global__ void __launch_bounds__(kThreads, 1)
     mqa_heads_kernel(const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ CUtensorMap box_c,
@@ -468,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The last stage holds the query block until the prologue is done.
       if (it == C::kStages - 1 && !wait_all(qready, 0, p, abort_flag)) break;
       const bool win = t >= tiles_c;
-      const bool gathered = !win && p.sel_idx != nullptr;
+      // Tiles that the transform warps fetch (every MXFP4 entry tile).
+      const bool gathered = !win && (kMx || p.sel_idx != nullptr);
       int32_t grow[2], rpos[2];
       bool valid[2];
 #pragma unroll
@@ -478,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j = t * TN + r;
           valid[hh] = j < n_c;
           int64_t i = j;
-          if (valid[hh] && gathered) {
+          if (valid[hh] && p.sel_idx != nullptr) {
             i = cur[hh];
             if (i < 0 || i >= n_vis) {
               report(p.status, CSA_ERR_DEVICE_INDEX);
@@ -530,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (*abort_flag && lane == 0) {  // box copies still in flight must land first
       for (int j = std::max(0, it - C::kStages); j < it; ++j)
-        if (t0 + j >= tiles_c || p.sel_idx == nullptr)
+        if (t0 + j >= tiles_c || (!kMx && p.sel_idx == nullptr))
           mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, p.status);
     }
     // A CTA whose tiles were all safe still waits once, so that the grid
@@ -639,20 +681,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    constexpr int kAhead = C::kStages - 1;
-    bool fetch_ok = true;
-    {
-      int64_t ri[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) ri[u] = u < ntile ? row_index(u) : 0;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (u < ntile && fetch_ok) fetch_ok = fetch(u, ri[u]);
-    }
-    int64_t nxt = kAhead < ntile ? row_index(kAhead) : 0;
-    for (int it = 0; it < ntile && fetch_ok; ++it) {
+    // One tile whose rows land in the stage as bf16: wait for them, zero the
+    // masked ones, normalise and rotate window tokens, hand the tile over.
+    auto transform = [&](int it) -> bool {
       const int s = it % C::kStages;
-      if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) break;
+      if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) return false;
       Meta& M = meta[s];
       uint8_t* st = stages + s * C::kStageBytes;
       const bool valid = (M.valid[r >> 5] >> (r & 31)) & 1u;
@@ -717,6 +750,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&ready[s]);
+      return true;
+    };
+    if constexpr (kMx) {
+      // MXFP4 entries: a thread holds whole blocks of 32 values (16 bytes of
+      // codes and their scale byte), the lanes of a row contiguous, fetched
+      // one tile ahead straight into registers; their bf16 values (exact)
+      // go into the stage.  64 rows are 17 KB against the 64 KB of bf16, and
+      // the conversion (about five instructions a pair of values) hides
+      // behind the half-rate MMAs of the tile before.
+      constexpr int kBlk = D / kMxBlock;       // blocks per row
+      constexpr int kU = TN * kBlk / 128;      // blocks per thread and tile
+      const int blk = tid % kBlk;
+      const uint8_t* seq = p.kv4 + (int64_t)b * p.N_cap * mx_row_bytes(D);
+      bool waited = sel_tiles;
+      auto issue = [&](int it, uint4 (&cd)[kU], uint32_t (&sc)[kU]) {
+        const int t = t0 + it;
+        if (it >= ntile || t >= tiles_c) return;
+        if (!waited && !tile_safe(t)) {
+          pdl_wait();
+          waited = true;
+        }
+        int64_t e[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int j = t * TN + u * (128 / kBlk) + tid / kBlk;
+          e[u] = j;
+          if (p.sel_idx) e[u] = j < p.kmax ? p.sel_idx[(int64_t)row * p.kmax + j] : -1;
+          if (j >= n_c || e[u] >= n_vis) e[u] = -1;  // masked: zeros
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          cd[u] = make_uint4(0u, 0u, 0u, 0u);
+          sc[u] = 0u;
+          if (e[u] >= 0) {
+            // (L2 only: a line may also hold a row that this call writes.)
+            const uint8_t* src = seq + e[u] * mx_row_bytes(D);
+            cd[u] = __ldcg(reinterpret_cast<const uint4*>(src) + blk);
+            sc[u] = __ldcg(src + D / 2 + blk);
+          }
+        }
+      };
+      auto tile = [&](int it, const uint4 (&cd)[kU], const uint32_t (&sc)[kU]) -> bool {
+        const int s = it % C::kStages;
+        mbar_arrive(&full[s]);
+        if (t0 + it >= tiles_c) return transform(it);
+        if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) return false;
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) top = max(top, sc[u]);
+        uint8_t* st = stages + s * C::kStageBytes;
+        if (__any_sync(0xffffffffu, top > 128u))
+          mx_store_tile<D, true>(st, tid, cd, sc);
+        else
+          mx_store_tile<D, false>(st, tid, cd, sc);
+        fence_proxy_async_smem();
+        mbar_arrive(&ready[s]);
+        return true;
+      };
+      uint4 ca[kU], cb[kU];
+      uint32_t sa[kU], sb[kU];
+      issue(0, ca, sa);
+      for (int it = 0; it < ntile; it += 2) {
+        issue(it + 1, cb, sb);
+        if (!tile(it, ca, sa) || it + 1 >= ntile) break;
+        issue(it + 2, ca, sa);
+        if (!tile(it + 1, cb, sb)) break;
+      }
+    } else {
+    constexpr int kAhead = C::kStages - 1;
+    bool fetch_ok = true;
+    {
+      int64_t ri[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) ri[u] = u < ntile ? row_index(u) : 0;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (u < ntile && fetch_ok) fetch_ok = fetch(u, ri[u]);
+    }
+    int64_t nxt = kAhead < ntile ? row_index(kAhead) : 0;
+    for (int it = 0; it < ntile && fetch_ok; ++it) {
+      if (!transform(it)) break;
       if (it + kAhead < ntile) {
         const int64_t cur = nxt;
         if (it + kAhead + 1 < ntile) nxt = row_index(it + kAhead + 1);
@@ -724,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     cp_async_wait_all();  // no copy may still target shared memory at exit
+    }
   } else {
     // ------------------------------------------------- softmax / epilogue --
     // The warp with TMEM lane quarter q serves heads 16q .. 16q+15 of this
@@ -1073,10 +1188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // on this device (S <= 8 portable, up to 16 with the non-portable cluster
 // size); 0 when none can.  Cached per (device, kernel variant, S).
 int clusters_resident(const void* kern, int variant, int S, size_t smem) {
-  static int cached[64][8][17] = {};  // 0 unknown, else count + 1
+  static int cached[64][16][17] = {};  // 0 unknown, else count + 1
   if (S < 2 || S > 16) return 0;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || variant < 0 || variant >= 8)
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || variant < 0 || variant >= 16)
     return 0;
   int& c = cached[dev][variant][S];
   if (c) return c - 1;
@@ -1106,7 +1221,7 @@ int clusters_resident(const void* kern, int variant, int S, size_t smem) {
   return c - 1;
 }
 
-template <int D, int R>
+template <int D, int R, bool kMx>
 cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   using C = MCfg<D>;
   Params p{};
@@ -1127,6 +1242,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   p.safe_pos = a.safe_pos;
   p.safe_fixed = a.safe_fixed;
   p.kv_c = reinterpret_cast<const __nv_bfloat16*>(a.kv_c);
+  p.kv4 = static_cast<const uint8_t*>(a.kv_c);
   p.kmax = a.kmax;
   p.gamma_q = a.gamma_q;
   p.gamma_kv = a.gamma_kv;
@@ -1149,18 +1265,22 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   cudaError_t e = make_tmap_2d(&map_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                (uint64_t)rows * a.H, D, TN, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  e = make_tmap_2d(&box_c, a.kv_c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.B * a.N_cap,
-                   D, TN, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
+  if constexpr (kMx) {
+    box_c = map_q;  // MXFP4 entries are not read through a map
+  } else {
+    e = make_tmap_2d(&box_c, a.kv_c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                     (uint64_t)a.B * a.N_cap, D, TN, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
   e = make_tmap_2d(&box_t, a.kv_tok, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.B * a.L_cap,
                    D, TN, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
 
   const size_t smem = 1024 + (size_t)C::kStages * C::kStageBytes + 2 * C::kPBytes +
                       C::kStages * sizeof(Meta) + 32 * 8 + 16 + 16 + 2 * D * sizeof(float);
-  auto kern = mqa_heads_kernel<D, R>;
-  const int variant = (D == 512 ? 0 : 3) + R / 32;
-  e = ensure_smem_attr(reinterpret_cast<const void*>(kern), 3 + variant, smem);
+  auto kern = mqa_heads_kernel<D, R, kMx>;
+  const int variant = (D == 512 ? 0 : 3) + R / 32 + (kMx ? 5 : 0);
+  e = ensure_smem_attr(reinterpret_cast<const void*>(kern), (kMx ? 16 : 3) + variant, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(cps * a.splits, rows, 1);
   // The splits of each head group form one cluster and merge in-kernel, when
@@ -1222,16 +1342,23 @@ cudaError_t launch_mqa_merge(const MqaLaunch& a, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_mqa(const MqaLaunch& a, cudaStream_t stream) {
+namespace {
+template <bool kMx>
+cudaError_t launch_shape(const MqaLaunch& a, cudaStream_t stream) {
   if (a.D == 512) {
-    if (a.rope_dim == 64) return launch_impl<512, 64>(a, stream);
-    if (a.rope_dim == 32) return launch_impl<512, 32>(a, stream);
-    if (a.rope_dim == 0) return launch_impl<512, 0>(a, stream);
+    if (a.rope_dim == 64) return launch_impl<512, 64, kMx>(a, stream);
+    if (a.rope_dim == 32) return launch_impl<512, 32, kMx>(a, stream);
+    if (a.rope_dim == 0) return launch_impl<512, 0, kMx>(a, stream);
   } else if (a.D == 128) {
-    if (a.rope_dim == 32) return launch_impl<128, 32>(a, stream);
-    if (a.rope_dim == 0) return launch_impl<128, 0>(a, stream);
+    if (a.rope_dim == 32) return launch_impl<128, 32, kMx>(a, stream);
+    if (a.rope_dim == 0) return launch_impl<128, 0, kMx>(a, stream);
   }
   return cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t launch_mqa(const MqaLaunch& a, cudaStream_t stream) {
+  return a.mx ? launch_shape<true>(a, stream) : launch_shape<false>(a, stream);
 }
 
 }  // namespace csa

@@ -1,0 +1,109 @@
+// MXFP4 on the device: blocks of 32 values share one power-of-two scale
+// (E8M0, byte e + 127), each value one E2M1 code (sign, two exponent bits,
+// one mantissa bit: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; the OCP
+// microscaling formats), two codes a byte, the even value in the low nibble.
+//
+// Quantisation (of bf16 values): e is the smallest integer with
+// max|x| <= 6 * 2^e, so no value saturates; codes round x * 2^-e to nearest,
+// ties to even.  x * 2^-e is exact in fp32 and every rounding border is a
+// representable number, so codes and scales are defined bit for bit.
+// Values (code * 2^e) are exact in bf16.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace csa {
+
+constexpr int kMxBlock = 32;
+
+// Scale byte of a block from the bf16 bits (sign cleared) of its largest
+// magnitude.  amax = 1.f * 2^k <= 6 * 2^e = 1.5 * 2^(e+2): e = k - 2, one more
+// when the fraction exceeds one half.  0 for a zero block; 255 (NaN) when a
+// value is NaN or infinite.
+CSA_DEV uint32_t mx_scale_byte(uint32_t amax) {
+  if (amax >= 0x7F80u) return 255u;
+  const int e = (int)(amax >> 7) - 2 + ((amax & 0x7Fu) > 0x40u ? 1 : 0);
+  return e > 0 ? (uint32_t)e : 0u;
+}
+
+// 2^(127 - byte), the factor that brings a block's values into E2M1 range
+// (0 for a NaN block, whose codes are all zero).
+CSA_DEV float mx_inv_scale(uint32_t byte) {
+  return byte >= 254u ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+
+// Eight fp32 values (already scaled) -> eight codes, value i in bits 4i.
+CSA_DEV uint32_t mx_codes8(const float (&x)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
+}
+
+// Eight bf16 values (pairs) of a block with scale byte `s` -> codes.
+CSA_DEV uint32_t mx_quantise8(const uint32_t (&w)[4], uint32_t s) {
+  const float f = mx_inv_scale(s);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = s == 255u ? 0.f : bf16_lo(w[i]) * f;
+    x[2 * i + 1] = s == 255u ? 0.f : bf16_hi(w[i]) * f;
+  }
+  return mx_codes8(x);
+}
+
+// Largest magnitude of eight bf16 values, as bf16 bits (integer order of the
+// magnitudes; NaN and infinity are the largest).
+CSA_DEV uint32_t mx_amax8(const uint32_t (&w)[4]) {
+  const uint32_t k = 0x7FFF7FFFu;
+  const uint32_t a = __vmaxu2(__vmaxu2(w[0] & k, w[1] & k), __vmaxu2(w[2] & k, w[3] & k));
+  return max(a & 0xFFFFu, a >> 16);
+}
+
+CSA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Scale factors of a block as bf16 pairs.  A code's exponent and mantissa
+// bits placed at bits 8..6 of a bf16 are its magnitude times 2^-126 (its zero
+// exponent becomes a bf16 subnormal, which the multiply keeps), so the value
+// is that times 2^126 * 2^(s-127) = 2^(s-1): one exact product for
+// s <= 128, and a second factor 2^(s-128) (NaN for s = 255) above.
+struct MxScale {
+  uint32_t lo, hi;
+  CSA_DEV explicit MxScale(uint32_t s) {
+    const uint32_t l = min(s, 128u);
+    lo = ((l + 126u) << 7) * 0x10001u;
+    hi = (s == 255u ? 0x7FC0u : (s - l + 127u) << 7) * 0x10001u;
+  }
+};
+
+// Eight codes (value i in bits 4i) -> eight bf16 values as four pairs.
+// kWide: scale bytes above 128 are possible (MxScale::hi is not one).
+// The high nibble of a byte of w << 4 (w) is the even (odd) code of its pair:
+// one byte permute puts both into the high bytes of the two halves, sign in
+// place and magnitude six bits too high.
+template <bool kWide>
+CSA_DEV void mx_values8(uint32_t w, const MxScale& sc, uint32_t (&o)[4]) {
+  const uint32_t v = w << 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // bytes: 1 = byte i of v, 3 = byte i of w (0 and 2 are masked away)
+    const uint32_t sel = (uint32_t)(i | (i << 4) | ((i + 4) << 8) | ((i + 4) << 12));
+    const uint32_t r = __byte_perm(v, w, sel);
+    const uint32_t x = (r & 0x80008000u) | ((r >> 6) & 0x01C001C0u);
+    o[i] = mul_bf16x2(x, sc.lo);
+    if (kWide) o[i] = mul_bf16x2(o[i], sc.hi);
+  }
+}
+
+}  // namespace csa

@@ -462,6 +462,121 @@ csa_status hca_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
                              int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The compressed cache in 4 bits (MXFP4).  The pages have no counterpart:
+ * this is this library's, for callers whose cache has to be smaller than
+ * bf16 (0.53 bytes a value instead of 2).
+ *
+ * Format (the OCP microscaling formats): blocks of 32 neighbouring values
+ * share one scale 2^e, stored as the byte e + 127 (E8M0); each value is an
+ * E2M1 code (sign, magnitude 0, 0.5, 1, 1.5, 2, 3, 4 or 6), two codes a
+ * byte, the even value in the low four bits.  A cache row of d values:
+ *   bytes 0 .. d/2-1           codes
+ *   bytes d/2 .. d/2+d/32-1    scale bytes
+ *   up to mxfp4_row_bytes(d)   padding, never written or read
+ * mxfp4_row_bytes(512) = 272, mxfp4_row_bytes(128) = 80; 0 for other d.
+ * A cache is kv4 [B, N_cap, mxfp4_row_bytes(d)] uint8 (device).
+ *
+ * Quantisation: e is the smallest integer (at least -127) with
+ * max|x| <= 6 * 2^e, so no value saturates; codes round x / 2^e to nearest,
+ * ties to the even code.  A block of zeros has the byte 0; a block that holds
+ * a NaN or an infinity has the byte 255 and reads back as NaN.  The result
+ * is defined bit for bit, and every stored value is exact in bf16.
+ *
+ * mxfp4_cache_write: rows rows[b, i, :] (i < count[b], at most n) of sequence
+ * b are quantised into entries first_entry[b] + i.  Other entries, and rows
+ * of the call past a sequence's count, are left as they were.
+ *   rows        [B] x [n, d] bf16 (device): sequence b starts at element
+ *               b * seq_stride (>= n*d, a multiple of 8)
+ *   first_entry [B] int64 (device) or NULL (0);  count [B] int64 or NULL (n)
+ * mxfp4_cache_read: the values of entries idx[b, i] (i < count[b]), or of
+ * first_entry[b] + i, as bf16 rows; rows past the count, and rows with index
+ * -1 (the padding of a selection), are left as they were.
+ *   idx  [B, n] int32 (device) or NULL;  rows [B, n, d] bf16 (written)
+ * Device errors (both): an entry outside the cache -> CSA_ERR_DEVICE_INDEX,
+ * skipped.  Only p->B, d, m, overlap, entry_offset and eps are checked; first
+ * entries and indices are local to the cache (entry_offset does not enter).
+ * ------------------------------------------------------------------------- */
+size_t mxfp4_row_bytes(int d);
+
+csa_status mxfp4_cache_write(const csa_params* p, const void* rows, int64_t seq_stride, int64_t n,
+                             const int64_t* first_entry, const int64_t* count, void* kv4,
+                             int64_t N_cap, int32_t* dev_status, void* stream);
+
+csa_status mxfp4_cache_read(const csa_params* p, const void* kv4, int64_t N_cap,
+                            const int32_t* idx, const int64_t* first_entry, const int64_t* count,
+                            int64_t n, void* rows, int32_t* dev_status, void* stream);
+
+/* Every call that writes or attends over the compressed cache, on a cache in
+ * 4 bits: the same arguments, order of work, workspace and errors as the call
+ * without the suffix, with kv4 in place of kv_c.
+ *   - Writing calls quantise each entry as the bf16 cache would hold it: the
+ *     bytes are those of mxfp4_cache_write on the bf16 entry.
+ *   - Attending calls use each entry's stored values (exact in bf16); window
+ *     tokens stay bf16.  An entry that reads back as NaN and is selected (or
+ *     visible, dense) makes its rows NaN; entries that are not selected are
+ *     never read.
+ *   - The indexer's keys are the E4M3 keys of the bf16 cache.
+ * The context split below takes bf16 caches only. */
+csa_status hca_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,
+                              const int64_t* ctx_len, const float* w_s, const float* b_pos,
+                              const float* gamma, int64_t first_block, int64_t n_blocks, void* kv4,
+                              int64_t N_cap, int32_t* dev_status, void* stream);
+
+csa_status csa_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,
+                              const int64_t* ctx_len, const float* w_s, const float* b_pos,
+                              const float* gamma, int64_t first_block, int64_t n_blocks, void* kv4,
+                              int64_t N_cap, const void* idx_tok, const float* w_s_idx,
+                              const float* b_pos_idx, uint8_t* idx_key, float* idx_scale,
+                              int32_t* dev_status, void* stream);
+
+csa_status sparse_mqa_decode_mxfp4(const csa_params* p, const void* q, const int64_t* pos_q,
+                                   const void* kv4, int64_t N_cap, const int32_t* topk_idx,
+                                   const int32_t* topk_cnt, const void* kv_tok, int64_t L_cap,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   void* out, float* lse, void* ws, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream);
+
+csa_status dense_mqa_decode_mxfp4(const csa_params* p, const void* q, const int64_t* pos_q,
+                                  const void* kv4, int64_t N_cap, const void* kv_tok,
+                                  int64_t L_cap, const float* sink, const float* gamma_q,
+                                  const float* gamma_kv, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, int32_t* dev_status, void* stream);
+
+csa_status csa_prefill_chunk_mxfp4(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                                   const void* idx_tok, int64_t L_cap, const float* w_s,
+                                   const float* b_pos, const float* gamma, const float* w_s_idx,
+                                   const float* b_pos_idx, void* kv4, uint8_t* idx_key,
+                                   float* idx_scale, int64_t N_cap, const void* q,
+                                   const uint8_t* q_idx, const float* q_scale, const float* w,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   int32_t* topk_idx, int32_t* topk_cnt, void* out, void* ws,
+                                   size_t ws_bytes, int32_t* dev_status, void* stream);
+
+csa_status csa_decode_step_mxfp4(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                                 const void* idx_tok, int64_t L_cap, const float* w_s,
+                                 const float* b_pos, const float* gamma, const float* w_s_idx,
+                                 const float* b_pos_idx, void* kv4, uint8_t* idx_key,
+                                 float* idx_scale, int64_t N_cap, const void* q,
+                                 const uint8_t* q_idx, const float* q_scale, const float* w,
+                                 const float* sink, const float* gamma_q, const float* gamma_kv,
+                                 int32_t* topk_idx, int32_t* topk_cnt, void* out, float* lse,
+                                 void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+csa_status hca_decode_step_mxfp4(const csa_params* p, const int64_t* pos_q, const void* kv_tok,
+                                 int64_t L_cap, const float* w_s, const float* b_pos,
+                                 const float* gamma, void* kv4, int64_t N_cap, const void* q,
+                                 const float* sink, const float* gamma_q, const float* gamma_kv,
+                                 void* out, float* lse, void* ws, size_t ws_bytes,
+                                 int32_t* dev_status, void* stream);
+
+csa_status hca_prefill_chunk_mxfp4(const csa_params* p, int64_t P, int T, const void* kv_tok,
+                                   int64_t L_cap, const float* w_s, const float* b_pos,
+                                   const float* gamma, void* kv4, int64_t N_cap, const void* q,
+                                   const float* sink, const float* gamma_q, const float* gamma_kv,
+                                   void* out, float* lse, void* ws, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Grouped output projection ("DeepSeek V4 technical report" (agentupdate.ai),
  * 混合注意力机制, item 分组输出投影: because the head dim is 512, the heads'
  * outputs are not projected straight back to the model dim d; the n_h heads

@@ -1,0 +1,377 @@
+"""GPU tests of the attention over a 4-bit (MXFP4) cache.
+
+A stored value is exact in bf16 and the tensor cores see the same bf16 tile
+either way, so the result over a 4-bit cache is, bit for bit, that of the bf16
+call over a cache holding the stored values: that is what most tests here ask.
+The fp64 oracle on those values checks both (the attention tolerance of
+gpuhelp)."""
+import numpy as np
+import pytest
+import torch
+
+import mxref
+from compressed_sparse_kv_04_b200 import binding, configs, synth
+from gpuhelp import assert_attention_close, assert_lse_close, bits16, f32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    binding.lib()
+
+
+class Case:
+    def __init__(self, B, d, H, R, W, m, pos, N_cap, k=0, seed=1, gains=False, scale=1.0,
+                 offset=0):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.p = binding.make_params(B, d, H=H, k=k, window=W, rope_dim=R, m=m, entry_offset=offset)
+        self.m, self.W, self.R, self.k = m, W, R, k
+        rows = torch.randn(B, N_cap, d, generator=g, device=DEV)
+        rows = (rows * rows.square().mean(-1, keepdim=True).rsqrt() * scale).bfloat16()
+        self.kv4 = binding.mxfp4_cache(self.p, N_cap)
+        binding.mxfp4_cache_write(self.p, rows, self.kv4)
+        self.pos = torch.tensor(pos, dtype=torch.int64, device=DEV)
+        L = max(pos) + 1
+        self.kv_tok = torch.randn(B, L, d, generator=g, device=DEV).bfloat16()
+        self.q = torch.randn(B, H, d, generator=g, device=DEV).bfloat16()
+        self.sink = torch.randn(H, generator=g, device=DEV)
+        self.gq = synth.gains(d, seed, DEV) if gains else None
+        self.gkv = synth.gains(d, seed + 1, DEV) if gains else None
+        self.sel = self.cnt = None
+        if k:
+            n_vis = [min(max((x + 1) // m - offset, 0), N_cap) for x in pos]
+            rng = np.random.default_rng(seed)
+            sel = np.full((B, k), -1, np.int32)
+            for b, v in enumerate(n_vis):
+                c = min(k, v)
+                sel[b, :c] = np.sort(rng.choice(v, c, replace=False)) if c else []
+            self.sel = torch.from_numpy(sel).to(DEV)
+            self.cnt = torch.tensor([min(k, v) for v in n_vis], dtype=torch.int32, device=DEV)
+
+    def values(self):
+        """The cache's stored values as a bf16 cache."""
+        out = torch.empty(*self.kv4.shape[:2], self.p.d, dtype=torch.bfloat16, device=DEV)
+        binding.mxfp4_cache_read(self.p, self.kv4, out)
+        return out
+
+    def run(self, cache, status=0, ws=None):
+        p, B = self.p, self.p.B
+        mx = cache.dtype == torch.uint8
+        out = torch.full((B, p.H, p.d), float("nan"), dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((B, p.H), float("nan"), device=DEV)
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        op = binding.OP_SPARSE_MQA if self.k else binding.OP_DENSE_MQA
+        ws = binding.workspace(p, op, 1, cache.shape[1]) if ws is None else ws
+        kw = dict(gamma_q=self.gq, gamma_kv=self.gkv, lse=lse, ws=ws, dev_status=st)
+        if self.k:
+            fn = binding.sparse_mqa_decode_mxfp4 if mx else binding.sparse_mqa_decode
+            fn(p, self.q, self.pos, cache, self.sel, self.cnt, self.kv_tok, self.sink, out, **kw)
+        else:
+            fn = binding.dense_mqa_decode_mxfp4 if mx else binding.dense_mqa_decode
+            fn(p, self.q, self.pos, cache, self.kv_tok, self.sink, out, **kw)
+        torch.cuda.synchronize()
+        assert st.item() == status, st.item()
+        return out, lse
+
+    def check(self, orc=None):
+        vals = self.values()
+        out, lse = self.run(self.kv4)
+        out2, lse2 = self.run(vals)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        if orc is not None:
+            B, p = self.p.B, self.p
+            ro, rl = orc.mqa(bits16(self.q).reshape(B, 1, p.H, p.d),
+                             self.pos.cpu().numpy().reshape(B, 1), bits16(vals), bits16(self.kv_tok),
+                             f32(self.sink), self.m, self.W, self.R,
+                             None if self.sel is None else self.sel.cpu().numpy().reshape(B, 1, -1),
+                             None if self.cnt is None else self.cnt.cpu().numpy().reshape(B, 1),
+                             None if self.gq is None else f32(self.gq),
+                             None if self.gkv is None else f32(self.gkv))
+            assert_attention_close(out.double().cpu().numpy(), ro[:, 0])
+            assert_lse_close(f32(lse), rl[:, 0], ro[:, 0],
+                             qnorm_gain=1.25 if self.gq is not None else 1.0)
+        return out, lse
+
+
+@pytest.mark.parametrize("d,R", [(512, 64), (512, 32), (512, 0), (128, 32), (128, 0)])
+@pytest.mark.parametrize("k", [0, 40])
+def test_against_the_oracle(orc, d, R, k):
+    """Lengths around tile edges, one sequence with a partial first block."""
+    Case(4, d, 128 if d == 512 else 16, R, 128, 4, [2, 255, 259, 700], 180, k=k, gains=R > 0).check(orc)
+
+
+@pytest.mark.parametrize("H", [1, 63, 64, 65, 128])
+def test_heads(orc, H):
+    Case(2, 512, H, 64, 100, 4, [3, 1000], 251, k=70, seed=H).check(orc)
+
+
+@pytest.mark.parametrize("W", [0, 1, 64, 200])
+def test_windows(orc, W):
+    """Also a row with nothing to attend (W = 0, no complete block): zeros."""
+    out, lse = Case(3, 128, 5, 32, W, 4, [1, 3, 90], 25, seed=W).check(orc)
+    if W == 0:
+        assert (out[0] == 0).all()
+
+
+def test_one_entry_capacity(orc):
+    Case(1, 512, 8, 64, 16, 4, [5], 1).check(orc)
+    Case(1, 512, 8, 64, 16, 4, [5], 1, k=1).check(orc)
+
+
+def test_many_splits_and_the_largest_selection():
+    Case(2, 512, 128, 64, 128, 4, [40000, 39000], 10001, k=2048).check()
+    Case(2, 512, 128, 64, 128, 4, [40000, 9000], 10001).check()
+    Case(9, 512, 64, 64, 128, 128, [70000 + i for i in range(9)], 600).check()
+    Case(80, 512, 64, 64, 128, 4, [900 + i for i in range(80)], 300, k=64).check()  # one split
+
+
+def test_large_scales():
+    """Entries whose scale bytes exceed 128 (values above 12)."""
+    c = Case(2, 512, 20, 64, 128, 4, [900, 800], 230, scale=40.0)
+    assert int(c.kv4[..., 256:272].max()) > 128
+    c.check()
+    Case(2, 512, 20, 64, 128, 4, [900, 800], 230, k=100, scale=40.0).check()
+    Case(2, 512, 20, 64, 128, 4, [900, 800], 230, k=100, scale=1e-30).check()
+
+
+def test_entry_offset():
+    Case(2, 512, 16, 64, 0, 4, [4 * 300 + 2, 4 * 120], 150, k=60, offset=100).check()
+    Case(2, 512, 16, 64, 0, 4, [4 * 300 + 2, 4 * 90], 150, offset=100).check()
+
+
+def test_unselected_and_invisible_entries_are_never_read():
+    """NaN entries that no row selects, or that lie past the visible ones,
+    change nothing; a selected one makes its rows NaN."""
+    c = Case(2, 512, 16, 64, 128, 4, [500, 700], 400, k=50)
+    ref = c.run(c.kv4)
+    keep = torch.zeros(2, 400, dtype=torch.bool, device=DEV)
+    for b in range(2):
+        keep[b, c.sel[b].long()] = True
+    poisoned = c.kv4.clone()
+    poisoned[~keep] = 255
+    got = c.run(poisoned)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    poisoned[1, c.sel[1, 7].long()] = 255
+    got = c.run(poisoned)
+    assert torch.equal(ref[0][0], got[0][0]) and torch.isnan(got[0][1].float()).all()
+    d = Case(2, 512, 16, 64, 128, 4, [500, 702], 400)
+    ref = d.run(d.kv4)
+    poisoned = d.kv4.clone()
+    poisoned[0, 125:] = 255
+    poisoned[1, 175:] = 255
+    got = d.run(poisoned)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
+def test_bad_indices_and_counts():
+    """Indices past the visible entries or below -1 are reported and skipped;
+    counts outside 0..k are clamped."""
+    c = Case(3, 512, 16, 64, 128, 4, [500, 700, 600], 400, k=50)
+    vals = c.values()
+    c.sel[0, 3], c.sel[1, 49], c.sel[2, 0] = 125, -5, 1 << 30
+    out, lse = c.run(c.kv4, status=7)
+    out2, lse2 = c.run(vals, status=7)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    c = Case(3, 512, 16, 64, 128, 4, [500, 700, 600], 400, k=50)
+    c.cnt[0], c.cnt[1] = -3, 0
+    out, lse = c.run(c.kv4)
+    out2, lse2 = c.run(c.values())
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_repeated_index_counts_twice(orc):
+    c = Case(1, 128, 8, 32, 32, 4, [600], 150, k=30)
+    c.sel[0, 10:20] = c.sel[0, 10]
+    c.check(orc)
+
+
+def test_two_streams_two_workspaces():
+    """Two calls at once, each with its own workspace, repeat each other."""
+    a = Case(2, 512, 128, 64, 128, 4, [9000, 7000], 2300, k=512, seed=3)
+    b = Case(2, 512, 128, 64, 128, 4, [9000, 7000], 2300, seed=4)
+    ra, rb = a.run(a.kv4)[0], b.run(b.kv4)[0]
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    wa = binding.workspace(a.p, binding.OP_SPARSE_MQA, 1, 2300)
+    wb = binding.workspace(b.p, binding.OP_DENSE_MQA, 1, 2300)
+    oa, ob = torch.empty_like(ra), torch.empty_like(rb)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        binding.sparse_mqa_decode_mxfp4(a.p, a.q, a.pos, a.kv4, a.sel, a.cnt, a.kv_tok, a.sink, oa,
+                                        ws=wa, stream=sa)
+        binding.dense_mqa_decode_mxfp4(b.p, b.q, b.pos, b.kv4, b.kv_tok, b.sink, ob, ws=wb,
+                                       stream=sb)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, ra) and torch.equal(ob, rb)
+
+
+def _step_inputs(w, L_cap):
+    kv_tok, idx_tok = synth.token_streams(w, L_cap=L_cap, device=DEV)
+    return kv_tok, idx_tok, synth.pool_params(w, DEV), (
+        synth.pool_params(w, DEV, indexer=True) if w.csa else None)
+
+
+def test_csa_decode_loop(orc):
+    """Write, index, select and attend, step by step: prompt compressed into the
+    4-bit cache, then six steps across block boundaries, captured into a graph
+    at the third.  The newest entry's bytes are those of the bf16 entry; the
+    attention is checked against the oracle on the stored values."""
+    w = configs.scaled(configs.CSA_128K, B=3, k=64, L=2048)
+    B, m, L_cap, N = 3, 4, 2048, 512
+    start = np.array([301, 514, 127])
+    kv_tok, idx_tok, (w_s, b_pos), (w_si, b_pi) = _step_inputs(w, L_cap)
+    p = binding.params_for(w, B=B)
+    kv4 = binding.mxfp4_cache(p, N)
+    key = torch.zeros(B, N, w.D_I, dtype=torch.uint8, device=DEV)
+    ksc = torch.zeros(B, N, device=DEV)
+    ctx = torch.from_numpy(start).to(DEV)
+    binding.csa_compress_mxfp4(p, kv_tok, ctx, w_s, b_pos, None, 0, N, kv4, idx_tok, w_si, b_pi, key,
+                               ksc)
+    kv_c = torch.zeros(B, N, w.d, dtype=torch.bfloat16, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pos = torch.empty(B, dtype=torch.int64, device=DEV)
+    qi = synth.queries(w, Q=1, device=DEV)
+    q, q_idx, q_sc, wt = (qi[n][:, 0].contiguous() for n in ("q", "q_idx", "q_scale", "w"))
+    out = torch.empty(B, w.H, w.D, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(B, w.H, device=DEV)
+    tidx = torch.empty(B, w.k, dtype=torch.int32, device=DEV)
+    tcnt = torch.empty(B, dtype=torch.int32, device=DEV)
+    ws = binding.workspace(p, binding.OP_CSA_DECODE_STEP, 1, N)
+    step = binding.CsaDecodeStep(p, kv_tok, idx_tok, w_s, b_pos, None, w_si, b_pi, kv4, key, ksc,
+                                 qi["sink"], tidx, tcnt, ws, dev_status=st)
+    graph = None
+    for n in range(6):
+        pos.copy_(torch.from_numpy(start + n))
+        if n < 2:
+            binding.csa_decode_step_mxfp4(p, pos, kv_tok, idx_tok, w_s, b_pos, None, w_si, b_pi, kv4,
+                                          key, ksc, q, q_idx, q_sc, wt, qi["sink"], tidx, tcnt, out,
+                                          lse=lse, ws=ws, dev_status=st)
+        elif n == 2:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                step(pos, q, q_idx, q_sc, wt, out, lse)
+        if graph is not None:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        at = (start + n) // m
+        for b in range(B):
+            binding.csa_compress(p, kv_tok, pos + 1, w_s, b_pos, None, int(at[b]), 1, kv_c)
+        stored = kv4.cpu().numpy()
+        for b in range(B):
+            ref = mxref.cache_rows(mxref.bf16_values(kv_c[b, at[b]]))
+            assert np.array_equal(stored[b, at[b]], ref), (n, b)
+        vals = torch.empty_like(kv_c)
+        binding.mxfp4_cache_read(p, kv4, vals)
+        ro, rl = orc.mqa(bits16(q).reshape(B, 1, w.H, w.D), (start + n).reshape(B, 1), bits16(vals),
+                         bits16(kv_tok), f32(qi["sink"]), m, w.W, w.rope_dim,
+                         tidx.cpu().numpy()[:, None], tcnt.cpu().numpy()[:, None])
+        assert_attention_close(out.double().cpu().numpy(), ro[:, 0], f"step {n}")
+        assert_lse_close(f32(lse), rl[:, 0], ro[:, 0])
+        assert tcnt.tolist() == [min(64, (x + n + 1) // m) for x in start]
+
+
+def test_hca_decode_loop(orc):
+    w = configs.scaled(configs.HCA_1M, B=2, L=1536)
+    B, m, N = 2, 128, 12
+    start = np.array([125, 640])
+    kv_tok, _, (w_s, b_pos), _ = _step_inputs(w, 1536)
+    p = binding.params_for(w, B=B)
+    kv4 = binding.mxfp4_cache(p, N)
+    binding.hca_compress_mxfp4(p, kv_tok, torch.from_numpy(start).to(DEV), w_s, b_pos, None, 0, N, kv4)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qi = synth.queries(w, Q=1, device=DEV)
+    q = qi["q"][:, 0].contiguous()
+    ws = binding.workspace(p, binding.OP_HCA_DECODE_STEP, 1, N)
+    step = binding.HcaDecodeStep(p, kv_tok, w_s, b_pos, None, kv4, qi["sink"], ws, dev_status=st)
+    for n in range(6):
+        pos = torch.from_numpy(start + n).to(DEV)
+        out = torch.empty(B, w.H, w.D, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(B, w.H, device=DEV)
+        if n % 2:
+            step(pos, q, out, lse)
+        else:
+            binding.hca_decode_step_mxfp4(p, pos, kv_tok, w_s, b_pos, None, kv4, q, qi["sink"], out,
+                                          lse=lse, ws=ws, dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        vals = torch.empty(B, N, w.d, dtype=torch.bfloat16, device=DEV)
+        binding.mxfp4_cache_read(p, kv4, vals)
+        ro, rl = orc.mqa(bits16(q).reshape(B, 1, w.H, w.D), (start + n).reshape(B, 1), bits16(vals),
+                         bits16(kv_tok), f32(qi["sink"]), m, w.W, w.rope_dim)
+        assert_attention_close(out.double().cpu().numpy(), ro[:, 0], f"step {n}")
+        assert_lse_close(f32(lse), rl[:, 0], ro[:, 0])
+    kv_c = torch.zeros(B, N, w.d, dtype=torch.bfloat16, device=DEV)
+    binding.hca_compress(p, kv_tok, torch.from_numpy(start + 6).to(DEV), w_s, b_pos, None, 0, N, kv_c)
+    for b in range(B):
+        n = (start[b] + 5) // m + 1
+        assert np.array_equal(kv4[b, :n].cpu().numpy(), mxref.cache_rows(mxref.bf16_values(kv_c[b, :n])))
+
+
+@pytest.mark.parametrize("P,T", [(0, 1), (0, 70), (256, 37)])
+def test_csa_prefill_chunk(orc, P, T):
+    w = configs.scaled(configs.CSA_128K, B=1, k=32)
+    m, L = 4, P + T
+    N = -(-L // m) + 1
+    kv_tok, idx_tok, (w_s, b_pos), (w_si, b_pi) = _step_inputs(w, L)
+    p = binding.params_for(w, B=1)
+    kv4 = binding.mxfp4_cache(p, N)
+    key = torch.zeros(1, N, w.D_I, dtype=torch.uint8, device=DEV)
+    ksc = torch.zeros(1, N, device=DEV)
+    if P:
+        binding.csa_compress_mxfp4(p, kv_tok, torch.tensor([P], device=DEV), w_s, b_pos, None, 0,
+                                   P // m, kv4, idx_tok, w_si, b_pi, key, ksc)
+    qi = synth.queries(w, Q=T, device=DEV)
+    out = torch.empty(T, w.H, w.D, dtype=torch.bfloat16, device=DEV)
+    tidx = torch.empty(T, w.k, dtype=torch.int32, device=DEV)
+    tcnt = torch.empty(T, dtype=torch.int32, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = binding.workspace(p, binding.OP_PREFILL, T, N)
+    binding.csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, None, w_si, b_pi, kv4, key,
+                                    ksc, qi["q"][0], qi["q_idx"][0], qi["q_scale"][0], qi["w"][0],
+                                    qi["sink"], tidx, tcnt, out, ws=ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    vals = torch.empty(1, N, w.d, dtype=torch.bfloat16, device=DEV)
+    binding.mxfp4_cache_read(p, kv4, vals)
+    pos = (P + np.arange(T)).reshape(1, T)
+    ro, _ = orc.mqa(bits16(qi["q"]), pos, bits16(vals), bits16(kv_tok), f32(qi["sink"]), m, w.W,
+                    w.rope_dim, tidx.cpu().numpy()[None], tcnt.cpu().numpy()[None])
+    assert_attention_close(out.double().cpu().numpy(), ro[0])
+    kv_c = torch.zeros(1, N, w.d, dtype=torch.bfloat16, device=DEV)
+    binding.csa_compress(p, kv_tok, torch.tensor([L], device=DEV), w_s, b_pos, None, 0, N, kv_c)
+    assert np.array_equal(kv4[0, : -(-L // m)].cpu().numpy(),
+                          mxref.cache_rows(mxref.bf16_values(kv_c[0, : -(-L // m)])))
+
+
+@pytest.mark.parametrize("P,T", [(0, 130), (256, 5)])
+def test_hca_prefill_chunk(orc, P, T):
+    w = configs.scaled(configs.HCA_1M, B=1)
+    m, L = 128, P + T
+    N = -(-L // m)
+    kv_tok, _, (w_s, b_pos), _ = _step_inputs(w, L)
+    p = binding.params_for(w, B=1)
+    kv4 = binding.mxfp4_cache(p, N)
+    if P:
+        binding.hca_compress_mxfp4(p, kv_tok, torch.tensor([P], device=DEV), w_s, b_pos, None, 0,
+                                   P // m, kv4)
+    qi = synth.queries(w, Q=T, device=DEV)
+    out = torch.empty(T, w.H, w.D, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(T, w.H, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = binding.workspace(p, binding.OP_HCA_PREFILL, T, N)
+    binding.hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, None, kv4, qi["q"][0], qi["sink"],
+                                    out, lse=lse, ws=ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    vals = torch.empty(1, N, w.d, dtype=torch.bfloat16, device=DEV)
+    binding.mxfp4_cache_read(p, kv4, vals)
+    ro, rl = orc.mqa(bits16(qi["q"]), (P + np.arange(T)).reshape(1, T), bits16(vals), bits16(kv_tok),
+                     f32(qi["sink"]), m, w.W, w.rope_dim)
+    assert_attention_close(out.double().cpu().numpy(), ro[0])
+    assert_lse_close(f32(lse), rl[0], ro[0])

@@ -1,0 +1,131 @@
+"""The 4-bit (MXFP4) calls without a device: the reference of the GPU tests
+against hand-worked values, and every refusal (nothing is launched: a call
+that passes its checks would need pointers, which no test here gives)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import mxref
+from compressed_sparse_kv_04_b200 import binding
+from compressed_sparse_kv_04_b200 import build as csa_build
+
+
+@pytest.fixture(scope="module")
+def L():
+    csa_build.build()
+    return binding.lib()
+
+
+def P(**kw):
+    base = dict(B=2, d=512, H=128, H_I=64, D_I=128, k=1024, window=128, rope_dim=64, m=4)
+    base.update(kw)
+    return binding.make_params(**base)
+
+
+def test_reference_rounds_ties_to_even_codes():
+    x = np.zeros(32)
+    x[:9] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -2.5]
+    codes, s = mxref.quantise(x)
+    assert s == [127]
+    assert codes[:9].tolist() == [0, 2, 2, 4, 4, 6, 6, 7, 12]
+    assert mxref.values(codes, s)[:9].tolist() == [0, 1, 1, 2, 2, 4, 4, 6, -2]
+
+
+def test_reference_scale_is_the_smallest_that_holds():
+    for amax, e in ((6.0, 0), (6.03125, 1), (3.0, -1), (3.015625, 0), (448.0, 7), (2.0 ** -126, -127)):
+        x = np.zeros(32)
+        x[3] = -amax
+        assert mxref.quantise(x)[1] == [e + 127], amax
+
+
+def test_reference_values_are_exact_in_bf16():
+    x = mxref.hard_rows(200, 128, 7)
+    codes, s = mxref.quantise(mxref.bf16_values(x))
+    v = mxref.values(codes, s)
+    back = torch.from_numpy(v).bfloat16().double().numpy()
+    assert np.array_equal(back[~np.isnan(v)], v[~np.isnan(v)])
+    # no value saturates: half a step of the largest binade at most
+    fin = np.isfinite(mxref.bf16_values(x)).reshape(200, -1, 32).all(-1)
+    err = np.abs(v - mxref.bf16_values(x)).reshape(200, -1, 32).max(-1)
+    assert (err[fin] <= np.exp2(s[fin].astype(float) - 127)).all()
+
+
+def test_row_bytes(L):
+    assert L.mxfp4_row_bytes(512) == 272 and L.mxfp4_row_bytes(128) == 80
+    assert L.mxfp4_row_bytes(64) == 0 and L.mxfp4_row_bytes(-1) == 0
+    with pytest.raises(binding.CsaError):
+        binding.mxfp4_row_bytes(96)
+
+
+def test_cache_write_refusals(L):
+    def call(p, rows=None, stride=512, n=1, first=None, count=None, kv4=None, N=8):
+        return L.mxfp4_cache_write(None if p is None else C.byref(p), rows, stride, n, first, count,
+                                   kv4, N, None, None)
+    assert call(None) == 1
+    assert call(P(d=256)) == 2
+    assert call(P(B=70000)) == 2
+    assert call(P(), n=-1) == 1
+    assert call(P(), N=0) == 1
+    assert call(P(), N=1 << 31) == 1
+    assert call(P(), n=0) == 0                      # nothing to do
+    assert call(P()) == 1 and b"rows is null" in L.csa_last_error()
+    assert call(P(), rows=8) == 1                   # alignment
+    assert call(P(), rows=16, stride=520, n=2) == 1  # rows of two sequences overlap
+    assert call(P(), rows=16, stride=516) == 1      # not a multiple of 8
+    assert call(P(), rows=16, stride=-512) == 1
+    assert call(P(), rows=16, first=4) == 1 and b"first_entry" in L.csa_last_error()
+    assert call(P(), rows=16, count=12) == 1 and b"count" in L.csa_last_error()
+    assert call(P(), rows=16) == 1 and b"kv4 is null" in L.csa_last_error()
+    assert call(P(), rows=16, kv4=24) == 1
+
+
+def test_cache_read_refusals(L):
+    def call(p, kv4=None, N=8, idx=None, first=None, count=None, n=1, rows=None):
+        return L.mxfp4_cache_read(None if p is None else C.byref(p), kv4, N, idx, first, count, n,
+                                  rows, None, None)
+    assert call(None) == 1
+    assert call(P(d=64)) == 2
+    assert call(P(), n=0) == 0
+    assert call(P()) == 1 and b"kv4 is null" in L.csa_last_error()
+    assert call(P(), kv4=16, idx=2) == 1
+    assert call(P(), kv4=16, idx=16, first=16, rows=16) == 1
+    assert b"exclude" in L.csa_last_error()
+    assert call(P(), kv4=16) == 1 and b"rows is null" in L.csa_last_error()
+
+
+def test_attention_refusals_name_the_4bit_cache(L):
+    p = P()
+    args = (16, 16, None, 8, 16, 16, 16, 8, 16, None, None, 16, None, None, 0, None, None)
+    assert L.sparse_mqa_decode_mxfp4(C.byref(p), *args) == 1
+    assert b"sparse_mqa_decode_mxfp4: kv4 is null" in L.csa_last_error()
+    args = (16, 16, None, 8, 16, 8, 16, None, None, 16, None, None, 0, None, None)
+    assert L.dense_mqa_decode_mxfp4(C.byref(p), *args) == 1
+    assert b"dense_mqa_decode_mxfp4: kv4 is null" in L.csa_last_error()
+    for kw in (dict(H=129), dict(rope_dim=63), dict(window=1025)):
+        p = P(**kw)
+        assert L.dense_mqa_decode_mxfp4(C.byref(p), *args) == 2, kw
+    p = P()
+    args = (16, 16, 16, 8, 16, 8, 16, None, None, 16, None, None, 0, None, None)
+    assert L.dense_mqa_decode_mxfp4(C.byref(p), *args) == 4  # no workspace
+
+
+def test_binding_checks_shapes_before_the_library():
+    p = P(d=128, rope_dim=32)
+    rows = torch.zeros(2, 3, 128, dtype=torch.bfloat16)
+    kv4 = torch.zeros(2, 8, 80, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_write(p, rows, kv4)                    # host tensors
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_write(p, rows.float(), kv4)
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_write(p, rows[:, :, :64], kv4)
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_write(p, rows.transpose(0, 1), kv4)
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_read(p, kv4, rows.float())
+    with pytest.raises(ValueError):
+        binding.mxfp4_cache_read(p, kv4[:, :, :72], rows)
+    with pytest.raises(TypeError):
+        binding.mxfp4_cache_read(p, kv4, None)
