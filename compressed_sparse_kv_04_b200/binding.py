@@ -302,11 +302,11 @@ def csa_decode_step(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos
 
 class CsaDecodeStep:
     """csa_decode_step (or, with a uint8 cache, csa_decode_step_mxfp4) for a
-    fixed set of sequences: the arguments that stay the same from step to step (token buffers, caches, weights, sink and
-    gains, the selection outputs, workspace and status word) are checked and
-    converted once; each call passes the step's positions, queries and
-    outputs.  Same C entry point and the same device-side work as
-    csa_decode_step (argument marshalling only)."""
+    fixed set of sequences: the arguments that stay the same from step to step
+    (token buffers, caches, weights, sink and gains, the selection outputs,
+    workspace and status word) are checked and converted once; each call
+    passes the step's positions, queries and outputs.  Same C entry point and
+    the same device-side work as the plain call (argument marshalling only)."""
 
     def __init__(self, p, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv_c, idx_key,
                  idx_scale, sink, topk_idx, topk_cnt, ws, gamma_q=None, gamma_kv=None,
@@ -468,74 +468,109 @@ def mxfp4_cache(p, N_cap, device=None):
                        device=device or torch.cuda.current_device())
 
 
+_ROW_BYTES = {}
+
+
+def _row_bytes(d):
+    n = _ROW_BYTES.get(d)
+    if n is None:
+        n = _ROW_BYTES[d] = mxfp4_row_bytes(d)
+    return n
+
+
 def _need(t, name, dtype, *shape):
-    """Pointer of a tensor that must have this dtype and shape (None: any
-    length) and sit on the current device; None passes."""
+    """Address of a tensor that must have this dtype and shape (None: any
+    length), be contiguous and sit on the current device; None passes."""
     if t is None:
         return None
+    # The usual case in few steps: a decode step makes a dozen of these checks.
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and
+            t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
     if t.dtype != dtype or t.dim() != len(shape) or any(
             n is not None and n != m for n, m in zip(shape, t.shape)):
         want = ", ".join("*" if n is None else str(n) for n in shape)
         raise ValueError(f"{name} must be {dtype} [{want}], not {t.dtype} {list(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return _ptr(t)
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _must(t, name, dtype, *shape):
-    """_need for a tensor whose shape the call itself reads."""
-    if t is None:
-        raise TypeError(f"{name}: expected a torch.Tensor, got None")
-    return _need(t, name, dtype, *shape)
+def _size(t, name, dim):
+    """Length of a dimension that the call itself reads."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
+    if t.dim() <= dim:
+        raise ValueError(f"{name} has {t.dim()} dimensions")
+    return t.shape[dim]
 
 
 def _need_cache(p, kv4):
-    return _must(kv4, "kv4", torch.uint8, p.B, None, mxfp4_row_bytes(p.d))
+    return _need(kv4, "kv4", torch.uint8, p.B, _size(kv4, "kv4", 1), _row_bytes(p.d))
+
+
+def _need_tok(p, kv_tok):
+    return _need(kv_tok, "kv_tok", torch.bfloat16, p.B, _size(kv_tok, "kv_tok", 1), p.d)
+
+
+def _status(dev_status):
+    return _need(dev_status, "dev_status", torch.int32, 1)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _is_mxfp4(p, kv_c, kv_tok):
     if kv_c.dtype != torch.uint8:
         return False
     _need_cache(p, kv_c)
-    _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d)
+    _need_tok(p, kv_tok)
     return True
 
 
 def _ws(ws):
-    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+    return _ptr(ws), 0 if ws is None else ws.nbytes
 
 
 def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
     """Quantises rows [B, n, d] (bf16; each sequence's rows contiguous) into
     entries first_entry[b] + i, i < count[b], of kv4."""
-    if not isinstance(rows, torch.Tensor) or rows.dim() != 3 or rows.dtype != torch.bfloat16 or \
-            rows.shape[0] != p.B or rows.shape[2] != p.d:
-        raise ValueError(f"rows must be bfloat16 [{p.B}, n, {p.d}]")
-    n = rows.shape[1]
-    if n and not rows[0].is_contiguous():
+    n = _size(rows, "rows", 1)
+    if rows.dtype != torch.bfloat16 or rows.shape != (p.B, n, p.d):
+        raise ValueError(f"rows must be bfloat16 [{p.B}, n, {p.d}], not {rows.dtype} "
+                         f"{list(rows.shape)}")
+    seq, row, one = rows.stride()
+    if n and (one != 1 or (n > 1 and row != p.d)):
         raise ValueError("each sequence's rows must be contiguous")
-    if not rows.is_cuda or rows.device.index != torch.cuda.current_device():
+    if not rows.is_cuda or rows.get_device() != torch.cuda.current_device():
         raise ValueError("rows must be on the current CUDA device")
-    stride = rows.stride(0) if p.B > 1 else n * p.d
+    stride = seq if p.B > 1 else n * p.d
     _check(lib().mxfp4_cache_write(
-        C.byref(p), C.c_void_p(rows.data_ptr()), stride, n,
-        _need(first_entry, "first_entry", torch.int64, p.B), _need(count, "count", torch.int64, p.B),
-        _need_cache(p, kv4), kv4.shape[1], _need(dev_status, "dev_status", torch.int32, 1),
-        _stream(stream)))
+        C.byref(p), rows.data_ptr(), stride, n,
+        _need(first_entry, "first_entry", torch.int64, p.B),
+        _need(count, "count", torch.int64, p.B),
+        _need_cache(p, kv4), kv4.shape[1], _status(dev_status),
+        _raw_stream(stream)))
 
 
 def mxfp4_cache_read(p, kv4, rows, idx=None, first_entry=None, count=None, dev_status=None,
                      stream=None):
     """The values of entries idx[b, i] (int32, -1 skipped) or first_entry[b] + i,
     i < count[b], of kv4 into rows [B, n, d] (bf16)."""
-    rp = _must(rows, "rows", torch.bfloat16, p.B, None, p.d)
+    rp = _need(rows, "rows", torch.bfloat16, p.B, _size(rows, "rows", 1), p.d)
     n = rows.shape[1]
     _check(lib().mxfp4_cache_read(
         C.byref(p), _need_cache(p, kv4), kv4.shape[1], _need(idx, "idx", torch.int32, p.B, n),
-        _need(first_entry, "first_entry", torch.int64, p.B), _need(count, "count", torch.int64, p.B),
-        n, rp, _need(dev_status, "dev_status", torch.int32, 1), _stream(stream)))
+        _need(first_entry, "first_entry", torch.int64, p.B),
+        _need(count, "count", torch.int64, p.B),
+        n, rp, _status(dev_status), _raw_stream(stream)))
 
 
 def _pool_args(p, w_s, b_pos, gamma):
@@ -557,9 +592,9 @@ def hca_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blo
                        dev_status=None, stream=None):
     """hca_compress into a 4-bit cache."""
     _check(lib().hca_compress_mxfp4(
-        C.byref(p), _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d), kv_tok.shape[1],
+        C.byref(p), _need_tok(p, kv_tok), kv_tok.shape[1],
         _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
-        n_blocks, _need_cache(p, kv4), kv4.shape[1], _ptr(dev_status), _stream(stream)))
+        n_blocks, _need_cache(p, kv4), kv4.shape[1], _status(dev_status), _raw_stream(stream)))
 
 
 def csa_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv4,
@@ -568,20 +603,21 @@ def csa_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blo
     """csa_compress into a 4-bit cache (indexer keys as csa_compress)."""
     L, N = kv_tok.shape[1], kv4.shape[1]
     _check(lib().csa_compress_mxfp4(
-        C.byref(p), _must(kv_tok, "kv_tok", torch.bfloat16, p.B, None, p.d), L,
+        C.byref(p), _need_tok(p, kv_tok), L,
         _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
         n_blocks, _need_cache(p, kv4), N,
         *_index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L, N),
-        _ptr(dev_status), _stream(stream)))
+        _status(dev_status), _raw_stream(stream)))
 
 
 def _mqa_inputs(p, rows, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse):
     """Checked pointers of the attention's tensors, `rows` queries."""
     bf, f32 = torch.bfloat16, torch.float32
     return dict(q=_need(q, "q", bf, rows, p.H, p.d), kv4=_need_cache(p, kv4),
-                kv_tok=_must(kv_tok, "kv_tok", bf, p.B, None, p.d),
+                kv_tok=_need_tok(p, kv_tok),
                 sink=_need(sink, "sink", f32, p.H), gq=_need(gamma_q, "gamma_q", f32, p.d),
-                gkv=_need(gamma_kv, "gamma_kv", f32, p.d), out=_need(out, "out", bf, rows, p.H, p.d),
+                gkv=_need(gamma_kv, "gamma_kv", f32, p.d),
+                out=_need(out, "out", bf, rows, p.H, p.d),
                 lse=_need(lse, "lse", f32, rows, p.H))
 
 
@@ -593,7 +629,7 @@ def sparse_mqa_decode_mxfp4(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink, 
         C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
         _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
         _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
-        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _ptr(dev_status), _stream(stream)))
+        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev_status), _raw_stream(stream)))
 
 
 def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, gamma_kv=None,
@@ -603,7 +639,7 @@ def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, ga
     _check(lib().dense_mqa_decode_mxfp4(
         C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
         a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
-        _ptr(dev_status), _stream(stream)))
+        _status(dev_status), _raw_stream(stream)))
 
 
 def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
@@ -620,8 +656,8 @@ def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx
         ik, isc, N, a["q"], _need(q_idx, "q_idx", torch.uint8, T, p.H_I, p.D_I),
         _need(q_scale, "q_scale", torch.float32, T, p.H_I), _need(w, "w", torch.float32, T, p.H_I),
         a["sink"], a["gq"], a["gkv"], _need(topk_idx, "topk_idx", torch.int32, T, p.k),
-        _need(topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws), _ptr(dev_status),
-        _stream(stream)))
+        _need(topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws), _status(dev_status),
+        _raw_stream(stream)))
 
 
 def hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
@@ -631,7 +667,7 @@ def hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, gamma, kv4, q, sink, ou
     _check(lib().hca_prefill_chunk_mxfp4(
         C.byref(p), P, T, a["kv_tok"], kv_tok.shape[1], *_pool_args(p, w_s, b_pos, gamma), a["kv4"],
         kv4.shape[1], a["q"], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
-        _ptr(dev_status), _stream(stream)))
+        _status(dev_status), _raw_stream(stream)))
 
 
 def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
@@ -651,7 +687,7 @@ def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx,
         _need(w, "w", torch.float32, p.B, p.H_I), a["sink"], a["gq"], a["gkv"],
         _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
         _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(ws),
-        _ptr(dev_status), _stream(stream)))
+        _status(dev_status), _raw_stream(stream)))
 
 
 def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
@@ -661,7 +697,7 @@ def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out
     _check(lib().hca_decode_step_mxfp4(
         C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
         *_pool_args(p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
-        a["gkv"], a["out"], a["lse"], *_ws(ws), _ptr(dev_status), _stream(stream)))
+        a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev_status), _raw_stream(stream)))
 
 
 # ------------------------------------------- context split over several devices --

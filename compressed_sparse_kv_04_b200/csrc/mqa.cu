@@ -74,7 +74,11 @@ namespace {
 
 constexpr int TN = 64;         // KV rows per tile
 constexpr int HC = 64;         // heads per CTA
-constexpr int kThreads = 320;  // 10 warps
+constexpr int kThreads = 320;  // 10 warps (an MXFP4 cache: 14, four more to transform)
+template <bool kMx>
+constexpr int kTransform = kMx ? 256 : 128;
+template <bool kMx>
+constexpr int kBlockThreads = kThreads - 128 + kTransform<kMx>;
 constexpr float kRescaleThreshold = 8.0f;
 
 template <int D>
@@ -141,44 +145,28 @@ CSA_DEV uint32_t tile_off(int r, int d) {
   return (uint32_t)(d >> 6) * (TN * 128u) + (lin ^ (((lin >> 7) & 7u) << 4));
 }
 
-// The 128 transform threads' blocks of an MXFP4 tile, as bf16 into the stage.
-// Thread tid holds block tid % (D/32) of rows tid / (D/32) + u * 4096/D: the
-// 16-byte units 4*(blk&1) .. +3 of the row's chunk blk/2.  The lanes of a row
-// write their units in rotated order, so that eight lanes fill eight
-// different units of the swizzled rows (no bank conflict).
-template <int D, bool kWide>
-CSA_DEV void mx_store_tile(uint8_t* st, int tid, const uint4 (&cd)[TN * D / 4096],
-                           const uint32_t (&sc)[TN * D / 4096]) {
-  constexpr int kBlk = D / kMxBlock;
-  const int blk = tid % kBlk, rot = (blk >> 1) & 3;
-#pragma unroll
-  for (int u = 0; u < TN * kBlk / 128; ++u) {
-    const int rr = u * (128 / kBlk) + tid / kBlk;
-    uint32_t w[4] = {cd[u].x, cd[u].y, cd[u].z, cd[u].w};
-    if (rot & 1) {
-      const uint32_t w0 = w[0];
-      w[0] = w[1];
-      w[1] = w[2];
-      w[2] = w[3];
-      w[3] = w0;
-    }
-    if (rot & 2) {
-      const uint32_t w0 = w[0], w1 = w[1];
-      w[0] = w[2];
-      w[1] = w[3];
-      w[2] = w0;
-      w[3] = w1;
-    }
-    const MxScale scale(sc[u]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t o[4];
-      mx_values8<kWide>(w[j], scale, o);
-      *reinterpret_cast<uint4*>(st + tile_off(rr, kMxBlock * blk + 8 * ((j + rot) & 3))) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+// The 256 transform threads' share of an MXFP4 tile: thread tid holds block
+// blk (32 values) of rows row + u * kStep.  Eight neighbouring lanes hold two
+// blocks of four rows: 32 contiguous bytes of each (one sector), and eight
+// different 16-byte units of the swizzled bf16 rows (no bank conflict).
+template <int D>
+struct MxTile {
+  static constexpr int kBlk = D / kMxBlock;        // blocks per row
+  static constexpr int kStep = kTransform<true> / kBlk;  // rows per unit of all threads
+  static constexpr int kU = TN / kStep;            // units per thread
+  int blk, row;
+  CSA_DEV explicit MxTile(int tid) {
+    const int w = tid >> 5, l = tid & 31;
+    if constexpr (D == 512) {
+      blk = (l & 1) + 2 * (l >> 3) + 8 * (w & 1);
+      row = ((l >> 1) & 3) + 4 * (w >> 1);
+    } else {
+      static_assert(D == 128, "D must be 512 or 128");
+      blk = (l & 1) + 2 * ((l >> 3) & 1);
+      row = ((l >> 1) & 3) + 4 * (l >> 4) + 8 * w;
     }
   }
-}
+};
 
 CSA_DEV uint64_t desc_k(uint32_t saddr) { return sdesc_sw128(saddr, 16, 1024); }
 CSA_DEV uint64_t desc_mn(uint32_t saddr) { return sdesc_sw128(saddr, TN * 128, 1024); }
@@ -330,11 +318,14 @@ __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int ro
 }
 
 template <int D, int R, bool kMx>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     mqa_heads_kernel(const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ CUtensorMap box_c,
                      const __grid_constant__ CUtensorMap box_t, const Params p) {
   using C = MCfg<D>;
+  constexpr int NT = kTransform<kMx>;       // transform threads
+  constexpr int W0 = 2 + NT / 32;           // first softmax warp
+  constexpr int NW = kBlockThreads<kMx> / 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -436,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + 128);  // producer + the transform threads
-      mbar_init(&ready[s], 128);
+      mbar_init(&full[s], 1 + NT);  // producer + the transform threads
+      mbar_init(&ready[s], NT);
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&pvdone[1], 1);
     mbar_init(qready, 128);
     mbar_init(drain, 1);
-    mbar_init(done, kThreads / 32);
+    mbar_init(done, NW);
     mbar_init(qfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -630,14 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(drain, 0, p.status);
     }
-  } else if (warp < 6) {
+  } else if (warp < W0) {
     // ----------------------------------------------------------- transform --
     // Two threads per tile row.  Window tokens: 1/rms(c_t) over the full row
     // and the KV gain in place.  Every real row: RoPE on the rotated dims.
-    const int tid = threadIdx.x - 64;  // 0..127
+    const int tid = threadIdx.x - 64;  // 0 .. NT-1
     const int r = tid >> 1, hf = tid & 1;
-    for (int i = tid; i < D; i += 128) gam_s[D + i] = p.gamma_kv ? __ldg(p.gamma_kv + i) : 1.f;
-    named_barrier_sync(2, 128);  // the transform warps
+    for (int i = tid; i < D; i += NT) gam_s[D + i] = p.gamma_kv ? __ldg(p.gamma_kv + i) : 1.f;
+    named_barrier_sync(2, NT);  // the transform warps
     if (sel_tiles) pdl_wait();  // selected rows are gathered here
     const int n_c = sel_tiles ? sel_count() : (p.sel_idx ? 0 : (int)n_vis);
     // Tile `it`: selected entries are fetched here (thread pair r gathers
@@ -686,6 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto transform = [&](int it) -> bool {
       const int s = it % C::kStages;
       if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) return false;
+      if (tid >= 128) {  // two threads a row here: the other warps pass
+        mbar_arrive(&ready[s]);
+        return true;
+      }
       Meta& M = meta[s];
       uint8_t* st = stages + s * C::kStageBytes;
       const bool valid = (M.valid[r >> 5] >> (r & 31)) & 1u;
@@ -754,68 +749,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if constexpr (kMx) {
       // MXFP4 entries: a thread holds whole blocks of 32 values (16 bytes of
-      // codes and their scale byte), the lanes of a row contiguous, fetched
-      // one tile ahead straight into registers; their bf16 values (exact)
-      // go into the stage.  64 rows are 17 KB against the 64 KB of bf16, and
-      // the conversion (about five instructions a pair of values) hides
-      // behind the half-rate MMAs of the tile before.
-      constexpr int kBlk = D / kMxBlock;       // blocks per row
-      constexpr int kU = TN * kBlk / 128;      // blocks per thread and tile
-      const int blk = tid % kBlk;
+      // codes and their scale byte), fetched one tile ahead straight into
+      // registers; their bf16 values (exact) go into the stage.  64 rows are
+      // 17 KB against 64 KB of bf16.  The conversion takes about five
+      // instructions a pair of values; its loop stays rolled (one block a
+      // turn, the registers shifted down), since the unrolled one waited on
+      // the instruction cache four issue slots out of five, and eight warps
+      // share it (8 sequences of 8192 entries: 81 us unrolled on four warps,
+      // 54 rolled, 47 on eight warps; 43 without the conversion).
+      using X = MxTile<D>;
+      const X x(tid);
       const uint8_t* seq = p.kv4 + (int64_t)b * p.N_cap * mx_row_bytes(D);
       bool waited = sel_tiles;
-      auto issue = [&](int it, uint4 (&cd)[kU], uint32_t (&sc)[kU]) {
-        const int t = t0 + it;
-        if (it >= ntile || t >= tiles_c) return;
-        if (!waited && !tile_safe(t)) {
-          pdl_wait();
-          waited = true;
-        }
-        int64_t e[kU];
+      uint4 cd[X::kU], nd[X::kU];
+      uint32_t sc[X::kU], ns[X::kU];
+#pragma unroll 1
+      for (int it = -1; it < ntile; ++it) {
+        // Fetch tile it + 1.
+        const int t = t0 + it + 1;
+        if (it + 1 < ntile && t < tiles_c) {
+          if (!waited && !tile_safe(t)) {
+            pdl_wait();
+            waited = true;
+          }
+          int64_t e[X::kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int j = t * TN + u * (128 / kBlk) + tid / kBlk;
-          e[u] = j;
-          if (p.sel_idx) e[u] = j < p.kmax ? p.sel_idx[(int64_t)row * p.kmax + j] : -1;
-          if (j >= n_c || e[u] >= n_vis) e[u] = -1;  // masked: zeros
-        }
+          for (int u = 0; u < X::kU; ++u) {
+            const int j = t * TN + x.row + u * X::kStep;
+            e[u] = j;
+            if (p.sel_idx) e[u] = j < p.kmax ? p.sel_idx[(int64_t)row * p.kmax + j] : -1;
+            if (j >= n_c || e[u] >= n_vis) e[u] = -1;  // masked: zeros
+          }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          cd[u] = make_uint4(0u, 0u, 0u, 0u);
-          sc[u] = 0u;
-          if (e[u] >= 0) {
-            // (L2 only: a line may also hold a row that this call writes.)
-            const uint8_t* src = seq + e[u] * mx_row_bytes(D);
-            cd[u] = __ldcg(reinterpret_cast<const uint4*>(src) + blk);
-            sc[u] = __ldcg(src + D / 2 + blk);
+          for (int u = 0; u < X::kU; ++u) {
+            nd[u] = make_uint4(0u, 0u, 0u, 0u);
+            ns[u] = 0u;
+            if (e[u] >= 0) {
+              // (L2 only: a line may also hold a row that this call writes.)
+              const uint8_t* src = seq + e[u] * mx_row_bytes(D);
+              nd[u] = __ldcg(reinterpret_cast<const uint4*>(src) + x.blk);
+              ns[u] = __ldcg(src + D / 2 + x.blk);
+            }
           }
         }
-      };
-      auto tile = [&](int it, const uint4 (&cd)[kU], const uint32_t (&sc)[kU]) -> bool {
-        const int s = it % C::kStages;
-        mbar_arrive(&full[s]);
-        if (t0 + it >= tiles_c) return transform(it);
-        if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) return false;
-        uint32_t top = 0;
+        if (it >= 0) {
+          const int s = it % C::kStages;
+          mbar_arrive(&full[s]);
+          if (t0 + it >= tiles_c) {
+            if (!transform(it)) break;
+          } else {
+            if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) break;
+            // Block blk of a row: units 4*(blk&1) .. +3 of chunk blk/2, the
+            // swizzle the same for all of the thread's rows.
+            uint8_t* at = stages + s * C::kStageBytes;
+            uint8_t* unit[4];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) top = max(top, sc[u]);
-        uint8_t* st = stages + s * C::kStageBytes;
-        if (__any_sync(0xffffffffu, top > 128u))
-          mx_store_tile<D, true>(st, tid, cd, sc);
-        else
-          mx_store_tile<D, false>(st, tid, cd, sc);
-        fence_proxy_async_smem();
-        mbar_arrive(&ready[s]);
-        return true;
-      };
-      uint4 ca[kU], cb[kU];
-      uint32_t sa[kU], sb[kU];
-      issue(0, ca, sa);
-      for (int it = 0; it < ntile; it += 2) {
-        issue(it + 1, cb, sb);
-        if (!tile(it, ca, sa) || it + 1 >= ntile) break;
-        issue(it + 2, ca, sa);
-        if (!tile(it + 1, cb, sb)) break;
+            for (int j = 0; j < 4; ++j) unit[j] = at + tile_off(x.row, kMxBlock * x.blk + 8 * j);
+#pragma unroll 1
+            for (int u = 0; u < X::kU; ++u) {
+              const uint32_t w[4] = {cd[0].x, cd[0].y, cd[0].z, cd[0].w};
+              const MxScale scale(sc[0]);
+              const bool wide = __any_sync(0xffffffffu, sc[0] > 128u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+                mx_values8(w[j], scale.lo, o);
+                if (wide) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], scale.hi);
+                }
+                *reinterpret_cast<uint4*>(unit[j]) = make_uint4(o[0], o[1], o[2], o[3]);
+                unit[j] += X::kStep * 128;
+              }
+#pragma unroll
+              for (int i = 0; i + 1 < X::kU; ++i) {
+                cd[i] = cd[i + 1];
+                sc[i] = sc[i + 1];
+              }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&ready[s]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < X::kU; ++u) {
+          cd[u] = nd[u];
+          sc[u] = ns[u];
+        }
       }
     } else {
     constexpr int kAhead = C::kStages - 1;
@@ -855,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // columns) writes 64 dims of both halves.  The rotated dims (the last R)
     // all sit in the last 64-dim chunk of half 1.
     {
-      for (int i = threadIdx.x - 192; i < D; i += 128)
+      for (int i = threadIdx.x - 32 * W0; i < D; i += 128)
         gam_s[i] = p.gamma_q ? __ldg(p.gamma_q + i) : 1.f;
       named_barrier_sync(1, 128);  // the softmax warps
       // The block is in the last stage (TMA, 128-byte swizzled chunks):
@@ -961,15 +981,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Meta& M = meta[s];
       const bool win = M.window != 0;
       const uint32_t vw = M.valid[hf];
-      // Logits (log2 domain); window columns times 1/rms(c_t).
+      // Logits (log2 domain); window columns times 1/rms(c_t).  Entry tiles
+      // without a masked row (most tiles of a long list) take packed
+      // arithmetic: the same products and the same chains of sums, in a third
+      // of the instructions.
+      const bool whole = !win && __all_sync(0xffffffffu, vw == 0xFFFFFFFFu);
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (whole) {
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float x = sv[j];
-        if (win) x *= M.rn[32 * hf + j];
-        x = ((vw >> j) & 1u) ? x * p.scale_log2 : -INFINITY;
-        sv[j] = x;
-        m4[j & 3] = fmaxf(m4[j & 3], x);
+        for (int j = 0; j < 32; j += 2) {
+          const float2 y = mul_f32x2(make_float2(sv[j], sv[j + 1]), sc2);
+          sv[j] = y.x;
+          sv[j + 1] = y.y;
+          m4[j & 3] = fmaxf(m4[j & 3], y.x);
+          m4[(j + 1) & 3] = fmaxf(m4[(j + 1) & 3], y.y);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float x = sv[j];
+          if (win) x *= M.rn[32 * hf + j];
+          x = ((vw >> j) & 1u) ? x * p.scale_log2 : -INFINITY;
+          sv[j] = x;
+          m4[j & 3] = fmaxf(m4[j & 3], x);
+        }
       }
       float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));  // the row's other half
@@ -1010,17 +1046,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = m_run != -INFINITY;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t pk[16];
+      if (whole && __all_sync(0xffffffffu, live)) {
+        const float2 nm2 = make_float2(-m_run, -m_run);
+        float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        float p0 = live ? fast_exp2(sv[j] - m_run) : 0.f;
-        float p1 = live ? fast_exp2(sv[j + 1] - m_run) : 0.f;
-        l4[j & 3] += p0;
-        l4[(j + 1) & 3] += p1;
-        if (win) {
-          p0 *= M.rn[32 * hf + j];
-          p1 *= M.rn[32 * hf + j + 1];
+        for (int j = 0; j < 32; j += 4) {
+          const float2 xa = add_f32x2(make_float2(sv[j], sv[j + 1]), nm2);
+          const float2 xb = add_f32x2(make_float2(sv[j + 2], sv[j + 3]), nm2);
+          const float2 pa = make_float2(fast_exp2(xa.x), fast_exp2(xa.y));
+          const float2 pb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
+          la = add_f32x2(la, pa);
+          lb = add_f32x2(lb, pb);
+          pk[j / 2] = pack_bf16(pa.x, pa.y);
+          pk[j / 2 + 1] = pack_bf16(pb.x, pb.y);
         }
-        pk[j / 2] = pack_bf16(p0, p1);
+        l4[0] = la.x;
+        l4[1] = la.y;
+        l4[2] = lb.x;
+        l4[3] = lb.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float p0 = live ? fast_exp2(sv[j] - m_run) : 0.f;
+          float p1 = live ? fast_exp2(sv[j + 1] - m_run) : 0.f;
+          l4[j & 3] += p0;
+          l4[(j + 1) & 3] += p1;
+          if (win) {
+            p0 *= M.rn[32 * hf + j];
+            p1 *= M.rn[32 * hf + j + 1];
+          }
+          pk[j / 2] = pack_bf16(p0, p1);
+        }
       }
       float ls = (l4[0] + l4[1]) + (l4[2] + l4[3]);
       ls += __shfl_xor_sync(0xffffffffu, ls, 16);
@@ -1179,7 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     const int nh = pair ? min(HC, p.H - hg0) : p.H;
     float* wsplit = reinterpret_cast<float*>(stages) + warp * 32;  // S <= 16 weights
-    for (int j = split + p.splits * warp; j < nh; j += p.splits * (kThreads / 32))
+    for (int j = split + p.splits * warp; j < nh; j += p.splits * NW)
       merge_head<D, R, 4, false>(p, row, hg0 + j, lane, wsplit);
   }
 }
@@ -1187,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // How many clusters of S attention CTAs (one per SM) can be resident at once
 // on this device (S <= 8 portable, up to 16 with the non-portable cluster
 // size); 0 when none can.  Cached per (device, kernel variant, S).
-int clusters_resident(const void* kern, int variant, int S, size_t smem) {
+int clusters_resident(const void* kern, int variant, int threads, int S, size_t smem) {
   static int cached[64][16][17] = {};  // 0 unknown, else count + 1
   if (S < 2 || S > 16) return 0;
   int dev = 0;
@@ -1202,7 +1258,7 @@ int clusters_resident(const void* kern, int variant, int S, size_t smem) {
   if (ok) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+      cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1288,12 +1344,14 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   // clusters would run in waves: the separate merge kernel is faster).
   if (!p.fused && !a.emit_partials &&
       (int64_t)cps * rows <=
-          clusters_resident(reinterpret_cast<const void*>(kern), variant, a.splits, smem)) {
+          clusters_resident(reinterpret_cast<const void*>(kern), variant, kBlockThreads<kMx>,
+                            a.splits, smem)) {
     p.cluster_merge = 1;
-    return launch_pdl(kern, grid, dim3(kThreads), smem, stream, a.splits, a.chained, map_q, box_c,
-                      box_t, p);
+    return launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, a.splits, a.chained, map_q,
+                      box_c, box_t, p);
   }
-  e = launch_pdl(kern, grid, dim3(kThreads), smem, stream, 0, a.chained, map_q, box_c, box_t, p);
+  e = launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, 0, a.chained, map_q, box_c,
+                 box_t, p);
   if (e != cudaSuccess) return e;
   if (p.fused) return cudaSuccess;  // the attention kernel finished the rows
   if (a.emit_partials) return cudaSuccess;  // the caller merges the partials

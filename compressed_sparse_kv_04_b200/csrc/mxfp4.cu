@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   for (int u = 0; u < kUnroll; ++u) {
     if (!live[u]) continue;
     uint32_t o[4];
-    mx_values8<true>(codes[u], MxScale(s[u]), o);
+    const MxScale scale(s[u]);
+    mx_values8(codes[u], scale.lo, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], scale.hi);
     *reinterpret_cast<uint4*>(dst + (c0 + u * kThreads) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }

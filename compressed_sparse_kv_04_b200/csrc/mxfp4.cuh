@@ -87,22 +87,18 @@ struct MxScale {
   }
 };
 
-// Eight codes (value i in bits 4i) -> eight bf16 values as four pairs.
-// kWide: scale bytes above 128 are possible (MxScale::hi is not one).
-// The high nibble of a byte of w << 4 (w) is the even (odd) code of its pair:
-// one byte permute puts both into the high bytes of the two halves, sign in
-// place and magnitude six bits too high.
-template <bool kWide>
-CSA_DEV void mx_values8(uint32_t w, const MxScale& sc, uint32_t (&o)[4]) {
+// Eight codes (value i in bits 4i) -> eight bf16 values times `lo` as four
+// pairs.  The high nibble of a byte of w << 4 (w) is the even (odd) code of
+// its pair: one byte permute puts both into the high bytes of the two halves,
+// sign in place and magnitude six bits too high.
+CSA_DEV void mx_values8(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
   const uint32_t v = w << 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // bytes: 1 = byte i of v, 3 = byte i of w (0 and 2 are masked away)
     const uint32_t sel = (uint32_t)(i | (i << 4) | ((i + 4) << 8) | ((i + 4) << 12));
     const uint32_t r = __byte_perm(v, w, sel);
-    const uint32_t x = (r & 0x80008000u) | ((r >> 6) & 0x01C001C0u);
-    o[i] = mul_bf16x2(x, sc.lo);
-    if (kWide) o[i] = mul_bf16x2(o[i], sc.hi);
+    o[i] = mul_bf16x2((r & 0x80008000u) | ((r >> 6) & 0x01C001C0u), lo);
   }
 }
 
