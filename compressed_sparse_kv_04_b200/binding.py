@@ -32,10 +32,12 @@ EXPORTS = ["csa_version", "csa_last_error", "csa_workspace_bytes", "hca_compress
            "mxfp4_row_bytes", "mxfp4_cache_write", "mxfp4_cache_read", "hca_compress_mxfp4",
            "csa_compress_mxfp4", "sparse_mqa_decode_mxfp4", "dense_mqa_decode_mxfp4",
            "csa_prefill_chunk_mxfp4", "hca_prefill_chunk_mxfp4", "csa_decode_step_mxfp4",
-           "hca_decode_step_mxfp4"]
+           "hca_decode_step_mxfp4", "mxfp4_scale_bytes", "mxfp4_quantize",
+           "grouped_out_proj_mxfp4", "grouped_out_proj_mxfp4_workspace_bytes"]
 # Entry points that return a size, not a status.
 _SIZES = ("csa_version", "csa_last_error", "csa_workspace_bytes",
-          "grouped_out_proj_workspace_bytes", "mxfp4_row_bytes")
+          "grouped_out_proj_workspace_bytes", "mxfp4_row_bytes", "mxfp4_scale_bytes",
+          "grouped_out_proj_mxfp4_workspace_bytes")
 
 
 class CsaError(RuntimeError):
@@ -118,6 +120,12 @@ def _declare(L):
     L.mxfp4_row_bytes.restype = sz
     L.mxfp4_cache_write.argtypes = [P, vp, i64, i64, vp, vp, vp, i64, vp, vp]
     L.mxfp4_cache_read.argtypes = [P, vp, i64, vp, vp, vp, i64, vp, vp, vp]
+    L.mxfp4_scale_bytes.argtypes = [i64, i64]
+    L.mxfp4_scale_bytes.restype = sz
+    L.mxfp4_quantize.argtypes = [i64, i64, vp, i64, vp, vp, vp]
+    L.grouped_out_proj_mxfp4_workspace_bytes.argtypes = [i32] * 6
+    L.grouped_out_proj_mxfp4_workspace_bytes.restype = sz
+    L.grouped_out_proj_mxfp4.argtypes = [i32] * 6 + [vp] * 8 + [sz, vp, vp]
     for name in EXPORTS:
         if name not in _SIZES:
             getattr(L, name).restype = i32
@@ -698,6 +706,71 @@ def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out
         C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
         *_pool_args(p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
         a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev_status), _raw_stream(stream)))
+
+
+def mxfp4_scale_bytes(rows, cols):
+    """Bytes of an operand's scale tiles."""
+    n = lib().mxfp4_scale_bytes(rows, cols)
+    if n == 0:
+        raise CsaError(2, lib().csa_last_error().decode())
+    return n
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """x [rows, cols] (bf16, each row contiguous) as an operand of the 4-bit
+    product: (codes [rows, cols/2], scale tiles), allocated when not given."""
+    rows, cols = _size(x, "x", 0), _size(x, "x", 1)
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or \
+            x.get_device() != torch.cuda.current_device():
+        raise ValueError("x must be bfloat16 [rows, cols] with contiguous rows, on the current "
+                         "CUDA device")
+    n = mxfp4_scale_bytes(rows, cols)
+    if codes is None:
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(lib().mxfp4_quantize(rows, cols, x.data_ptr(), x.stride(0) if rows > 1 else cols,
+                                _need(codes, "codes", torch.uint8, rows, cols // 2),
+                                _need_scales(scales, "scales", n), _raw_stream(stream)))
+    return codes, scales
+
+
+def _need_scales(t, name, n):
+    """Scale tiles: `n` bytes in any shape."""
+    if isinstance(t, torch.Tensor) and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} bytes, not {t.numel()}")
+    return _need(t, name, torch.uint8, *(t.shape if isinstance(t, torch.Tensor) else ()))
+
+
+def grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model):
+    n = lib().grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model)
+    if n == 0:
+        raise CsaError(2, lib().csa_last_error().decode())
+    return n
+
+
+def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None, dev_status=None,
+                           stream=None):
+    """grouped_out_proj with 4-bit weights and activations: o [T, H, D] bf16,
+    w_g [g, d_g, H/g*D/2] and w_o [d_model, g*d_g/2] codes with their scale
+    tiles (mxfp4_quantize).  The workspace is allocated here when not given."""
+    if not isinstance(o, torch.Tensor) or o.dim() != 3:
+        raise ValueError("o must be [T, H, D]")
+    T, H, D = o.shape
+    g, d_g = _size(w_g, "w_g", 0), _size(w_g, "w_g", 1)
+    d_model = _size(w_o, "w_o", 0)
+    if ws is None:
+        ws = torch.empty(grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model),
+                         dtype=torch.uint8, device=o.device)
+    k1, k2 = H // max(g, 1) * D, g * d_g
+    u8, bf = torch.uint8, torch.bfloat16
+    _check(lib().grouped_out_proj_mxfp4(
+        T, H, D, g, d_g, d_model, _need(o, "o", bf, T, H, D), _need(w_g, "w_g", u8, g, d_g, k1 // 2),
+        _need_scales(w_g_scale, "w_g_scale", -(-k2 // 128) * (k1 // 128) * 512),
+        _need(w_o, "w_o", u8, d_model, k2 // 2),
+        _need_scales(w_o_scale, "w_o_scale", -(-d_model // 128) * (k2 // 128) * 512),
+        _need(y, "y", bf, T, k2), _need(z, "z", bf, T, d_model), _ptr(ws), ws.nbytes,
+        _status(dev_status), _raw_stream(stream)))
 
 
 # ------------------------------------------- context split over several devices --

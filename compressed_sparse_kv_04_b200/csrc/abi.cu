@@ -1201,6 +1201,148 @@ csa_status grouped_out_proj(int T, int H, int D, int g, int d_g, int d_model, co
   return CSA_OK;
 }
 
+// ------------------------------------------ grouped output projection, MXFP4 --
+size_t mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+  if (rows < 1 || cols < 128 || cols % 128 || rows > (int64_t)65535 * 128 || cols > (1 << 24)) {
+    fail(CSA_ERR_UNSUPPORTED_SHAPE,
+         "mxfp4_scale_bytes: rows=%lld cols=%lld (supported: rows 1..%d, cols a multiple of 128)",
+         (long long)rows, (long long)cols, 65535 * 128);
+    return 0;
+  }
+  return (size_t)((rows + 127) / 128) * (size_t)(cols / 128) * 512;
+}
+
+csa_status mxfp4_quantize(int64_t rows, int64_t cols, const void* x, int64_t ld, void* codes,
+                          void* scales, void* stream) {
+  const char* fn = "mxfp4_quantize";
+  if (rows == 0) return CSA_OK;
+  if (mxfp4_scale_bytes(rows, cols) == 0) return CSA_ERR_UNSUPPORTED_SHAPE;
+  if (ld < cols || ld % 8 || ld > ((int64_t)1 << 40))
+    return fail(CSA_ERR_INVALID_ARG, "%s: ld=%lld must be a multiple of 8 and at least cols", fn,
+                (long long)ld);
+  REQ_PTR(x);
+  REQ_PTR(codes);
+  REQ_PTR(scales);
+  cudaError_t e = csa::launch_mx_quantise(x, ld, rows, cols, codes, scales,
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return CSA_OK;
+}
+
+static csa_status check_proj_mx(const char* fn, int T, int H, int D, int g, int d_g, int d_model) {
+  csa_status st = check_proj(fn, T, H, D, g, d_g, d_model);
+  if (st != CSA_OK) return st;
+  if ((int64_t)(H / g) * D % 256 || (int64_t)g * d_g % 256)
+    return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: need (H/g)*D and g*d_g multiples of 256", fn);
+  if (T > 65535 * 128) return fail(CSA_ERR_UNSUPPORTED_SHAPE, "%s: T=%d too large", fn, T);
+  return CSA_OK;
+}
+
+// Workspace: the operands of o and y (codes, scale tiles), the partials.
+struct ProjPlanMx {
+  csa::MxGemmPlan a, b;
+  size_t oq, os, yq, ys, part;
+  size_t total() const { return oq + os + yq + ys + part + 256; }
+};
+
+static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g, int d_model) {
+  ProjPlanMx pl{};
+  const int64_t hd = (int64_t)H * D, k2 = (int64_t)g * d_g;
+  const int sms = csa::device_sm_count();
+  pl.a = csa::mx_gemm_plan(T, d_g, g, (int)(hd / g), sms);
+  pl.b = csa::mx_gemm_plan(T, d_model, 1, (int)k2, sms);
+  pl.oq = round_up((size_t)T * hd / 2, 256);
+  pl.os = mxfp4_scale_bytes(T, hd);
+  pl.yq = round_up((size_t)T * k2 / 2, 256);
+  pl.ys = mxfp4_scale_bytes(T, k2);
+  const size_t p1 = pl.a.partials ? (size_t)pl.a.splits * T * k2 * 4 : 0;
+  const size_t p2 = pl.b.partials ? (size_t)pl.b.splits * T * d_model * 4 : 0;
+  pl.part = round_up(p1 > p2 ? p1 : p2, 256);
+  return pl;
+}
+
+size_t grouped_out_proj_mxfp4_workspace_bytes(int T, int H, int D, int g, int d_g, int d_model) {
+  if (check_proj_mx("grouped_out_proj_mxfp4_workspace_bytes", T, H, D, g, d_g, d_model) != CSA_OK)
+    return 0;
+  return proj_plan_mx(T, H, D, g, d_g, d_model).total();
+}
+
+csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_model, const void* o,
+                                  const void* w_g, const void* w_g_scale, const void* w_o,
+                                  const void* w_o_scale, void* y, void* z, void* ws,
+                                  size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const char* fn = "grouped_out_proj_mxfp4";
+  csa_status st = check_proj_mx(fn, T, H, D, g, d_g, d_model);
+  if (st != CSA_OK) return st;
+  REQ_PTR(o);
+  REQ_PTR(w_g);
+  REQ_PTR(w_g_scale);
+  REQ_PTR(w_o);
+  REQ_PTR(w_o_scale);
+  OPT_PTR(y);
+  REQ_PTR(z);
+  OPT_PTR4(dev_status);
+  const ProjPlanMx pl = proj_plan_mx(T, H, D, g, d_g, d_model);
+  const size_t need = pl.total();
+  if (!ws || ws_bytes < need)
+    return fail(CSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                ws ? ws_bytes : (size_t)0);
+  if (!aligned16(ws)) return fail(CSA_ERR_INVALID_ARG, "%s: ws is not 16-byte aligned", fn);
+  char* oq = static_cast<char*>(ws);
+  char* os = oq + pl.oq;
+  char* yq = os + pl.os;
+  char* ys = yq + pl.yq;
+  float* part = reinterpret_cast<float*>(ys + pl.ys);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t hd = (int64_t)H * D, k2 = (int64_t)g * d_g;
+  // 1. o per token in 4 bits.
+  cudaError_t e = csa::launch_mx_quantise(o, hd, T, hd, oq, os, s);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  // 2. y = o W_g^T per group, quantised for the second product.
+  csa::MxGemm a{};
+  a.tok = oq;
+  a.tok_scale = os;
+  a.tok_k = hd;
+  a.w = w_g;
+  a.w_scale = w_g_scale;
+  a.K = (int)(hd / g);
+  a.N = d_g;
+  a.groups = g;
+  a.T = T;
+  a.tok_m = pl.a.tok_m;
+  a.bn = pl.a.bn;
+  a.splits = pl.a.splits;
+  a.part = pl.a.partials ? part : nullptr;
+  a.c = y;
+  a.yq = yq;
+  a.ys = ys;
+  a.status = dev_status;
+  a.chained = 1;
+  e = csa::launch_mx_gemm(a, s);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  // 3. z = y W_o^T.
+  csa::MxGemm b{};
+  b.tok = yq;
+  b.tok_scale = ys;
+  b.tok_k = k2;
+  b.w = w_o;
+  b.w_scale = w_o_scale;
+  b.K = (int)k2;
+  b.N = d_model;
+  b.groups = 1;
+  b.T = T;
+  b.tok_m = pl.b.tok_m;
+  b.bn = pl.b.bn;
+  b.splits = pl.b.splits;
+  b.part = pl.b.partials ? part : nullptr;
+  b.c = z;
+  b.status = dev_status;
+  b.chained = 1;
+  e = csa::launch_mx_gemm(b, s);
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return CSA_OK;
+}
+
 // ----------------------------------------- context split over several devices --
 csa_status csa_shard_candidates(const csa_params* p, int Q, const float* scores, int64_t N_cap,
                                 const int32_t* topk_idx, const int32_t* topk_cnt,

@@ -213,6 +213,39 @@ struct MxCacheLaunch {
 cudaError_t launch_mx_cache_write(const MxCacheLaunch& c, cudaStream_t stream);
 cudaError_t launch_mx_cache_read(const MxCacheLaunch& c, cudaStream_t stream);
 
+// Rows [rows, cols] of bf16 (ld elements apart) -> MXFP4 operand: codes
+// [rows, cols/2] and scale tiles [ceil(rows/128), cols/128, 512] (cols a
+// multiple of 128).
+cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t cols, void* codes,
+                               void* scales, cudaStream_t stream);
+
+// One product of the MXFP4 grouped projection: for each group j,
+// C[t, j*N + n] = sum_k tok[t, j*K + k] * W[j*N + n, k], fp32 accumulation,
+// rounded to bf16 (c, may be null with yq) and, with yq, quantised into the
+// operand (yq, ys) of the next product.
+struct MxGemmPlan {
+  int tok_m;       // tokens are the MMA's rows (else weights)
+  int bn;          // the MMA's N
+  int splits;      // K splits
+  int partials;    // fp32 partials [splits, T, groups*N] are needed
+};
+MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms);
+struct MxGemm {
+  const void* tok;        // codes [T, tok_k/2]
+  const void* tok_scale;  // scale tiles
+  int64_t tok_k;          // values per token (groups * K)
+  const void* w;          // codes [groups*N, K/2]
+  const void* w_scale;    // scale tiles
+  int K, N, groups, T;
+  int tok_m, bn, splits;  // see MxGemmPlan
+  float* part;            // partials, or null (tok_m and splits == 1)
+  void* c;
+  void *yq, *ys;
+  int32_t* status;
+  int chained;            // see launch_pdl
+};
+cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t stream);
+
 int device_sm_count();
 
 // Launches `kern` and, when cluster_x > 0, as (cluster_x, 1, 1) clusters.
@@ -268,7 +301,7 @@ csa_status set_error(csa_status s, const char* fmt, ...);
 // is then skipped, which keeps launches legal inside CUDA-graph capture).
 // `slot` (0..31) identifies the kernel: each kernel instance has its own
 // (indexer 0-1, 15-16 and 19-20, top-k 2, 8-9 and 17, attention 3-7 and (over
-// an MXFP4 cache) 21-25, projection 10-14).
+// an MXFP4 cache) 21-25, projection 10-14 and (MXFP4) 26-31).
 cudaError_t ensure_smem_attr(const void* func, int slot, size_t bytes);
 
 }  // namespace csa

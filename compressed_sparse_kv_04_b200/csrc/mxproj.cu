@@ -1,0 +1,544 @@
+// Grouped output projection in MXFP4 (see mxfp4.cuh for the format): weights
+// held in 4 bits, activations quantised per token in blocks of 32 along the
+// inner dimension, products on the 5th-generation tensor cores with their
+// block scales (tcgen05.mma kind::mxf4), fp32 accumulation.
+//
+//   y[t, j*d_g + r] = bf16( sum_c W_g[j, r, c] * q(o)[t, j*H/g*D + c] )
+//   z[t, n]         = bf16( sum_i W_o[n, i]    * q(y)[t, i] )
+//
+// with q() the quantisation to MXFP4.  (The passages and the bf16 form: see
+// proj.cu.)
+//
+// One operand layout serves weights and activations: codes [rows, K/2]
+// row-major, loaded by TMA (128 bytes = 256 values a row and chunk, 128-byte
+// swizzle), and scale bytes in tiles of 128 rows x 4 blocks (512 bytes: byte
+// (r % 32) * 16 + (r % 128) / 32 * 4 + block % 4), the form in which
+// tcgen05.cp brings them to tensor memory (32 lanes x 16 bytes, replicated to
+// the four lane quarters): row r's four bytes sit in lane r % 32, column
+// r / 32.
+//
+// A chunk of 256 K values is 4 MMAs of K = 64.  Each ring stage has its own
+// scale columns in tensor memory, so a stage's copies are issued only after
+// the MMAs that read its former scales have completed (its `full` barrier
+// follows its `empty` barrier).
+//
+// Two forms of one kernel:
+//   - few tokens (T <= 128): weights are the MMA's M = 128 rows, tokens its N.
+//     The weights' bytes bound it: K is split so that two CTAs on every SM
+//     stream them; fp32 partials are summed by the kernel that quantises y
+//     (or stores z).
+//   - more tokens: tokens are the M = 128 rows, weights N = 128 or 256, so
+//     that a thread of the epilogue holds one token's neighbouring features
+//     and quantises y in registers.
+#include <algorithm>
+
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "tma.h"
+
+namespace csa {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int BM = 128;         // rows of the MMA's A operand
+constexpr int KB = 128;         // bytes of a row and chunk (256 values)
+constexpr int kScaleTile = 512; // scale bytes of 128 rows x 128 values
+
+CSA_DEV uint64_t desc_kmaj(uint32_t saddr) { return sdesc_sw128(saddr, 16, 1024); }
+
+// Scale tile in shared memory: 32 rows of 16 bytes, no swizzle (8-row groups
+// 128 bytes apart).
+CSA_DEV uint64_t desc_scale(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// kind::mxf4 (E2M1 operands, E8M0 scales per 32 values, K = 64, K-major,
+// fp32 accumulator); `id` selects the half (0 or 2) of the 4 scale bytes.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int id) {
+  return ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 4) << 24) | ((uint32_t)id << 29);
+}
+
+CSA_DEV void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                      uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;"
+      "\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+      : "memory");
+}
+
+// 512 bytes of shared memory -> 4 columns of 32 lanes, in every lane quarter.
+CSA_DEV void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// `bytes` (a multiple of 16) of global memory into shared memory, on bar.
+CSA_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+struct GemmArgs {
+  const uint8_t* tok_scale;  // token scale tiles [ceil(T/128), tok_k/128, 512]
+  const uint8_t* w_scale;    // weight scale tiles [w_rows/128, K/128, 512]
+  int T, chunks;             // tokens; K chunks per group
+  int64_t tok_tiles, w_tiles;  // scale tiles per 128 rows (of all groups; of one)
+  int groups_k;              // token chunks between groups (= chunks)
+  int N, splits, ldc;        // output features per group; K splits; features in all
+  float* part;               // [splits, T, ldc] fp32, or
+  __nv_bfloat16* c;          // [T, ldc] bf16 or null, and with yq != null
+  uint8_t* yq;               // codes [T, ldc/2] and
+  uint8_t* ys;               // scale tiles [ceil(T/128), ldc/128, 512] of the bf16 values
+  int32_t* status;
+};
+
+template <int BN, bool kTokM>
+struct Cfg {
+  static constexpr int kSB = BN > 128 ? 2 : 1;             // 128-row scale tiles of B
+  static constexpr int kABytes = BM * KB;
+  static constexpr int kBBytes = BN * KB;
+  static constexpr int kScaleBytes = (1 + kSB) * 2 * kScaleTile;
+  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
+  // One CTA per SM at BN = 256, else two.
+  static constexpr int kCtas = BN > 128 ? 1 : 2;
+  static constexpr int kStages = (kCtas == 1 ? 208 : 103) * 1024 / kStageBytes;
+  static constexpr int kScaleCols = (1 + kSB) * 8;         // columns of a stage's scales
+  static constexpr int kCols0 = (BN < 32 ? 32 : BN) + kStages * kScaleCols;
+  static constexpr uint32_t kCols = kCols0 <= 128 ? 128 : (kCols0 <= 256 ? 256 : 512);
+  static_assert(kStages >= 2 && kCols0 <= 512 && kCtas * (int)kCols <= 512, "tensor memory");
+};
+
+template <int BN, bool kTokM>
+__global__ void __launch_bounds__(kThreads)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap map_tok,
+                   const __grid_constant__ CUtensorMap map_w, const GemmArgs p) {
+  using C = Cfg<BN, kTokM>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  // Codes first (1024-byte aligned), then every stage's scale tiles.
+  uint8_t* scales = smem + C::kStages * (C::kABytes + C::kBBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kStages * C::kScaleBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* accf = empty + C::kStages;  // the accumulator is complete
+  uint64_t* drain = accf + 1;           // issued MMAs finished (abort path)
+  uint64_t* done = drain + 1;           // one arrival per warp when its role is over
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int group = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
+  // The chunks [k0, k1) of the group's inner dimension.
+  const int k0 = (int)((int64_t)p.chunks * split / p.splits);
+  const int nk = (int)((int64_t)p.chunks * (split + 1) / p.splits) - k0;
+  const int w_tile = kTokM ? BN : BM, t_tile = kTokM ? BM : BN;
+  const int n0 = blockIdx.x * w_tile;   // first feature within the group
+  const int t0 = blockIdx.y * t_tile;   // first token
+  const int w_row = group * p.N + n0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(drain, 1);
+    mbar_init(done, kThreads / 32);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_scale = tmem + (BN < 32 ? 32 : BN);
+  pdl_trigger();  // the next kernel may set itself up while this one runs
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer --
+    // Weights are caller inputs: the first ring's worth is requested before
+    // the wait on the previous kernel, which writes the tokens' operand.
+    if (elect_one()) {
+      tma_prefetch_desc(&map_tok);
+      tma_prefetch_desc(&map_w);
+      constexpr int kS = C::kStages;
+      constexpr int kWS = kTokM ? C::kSB : 1, kTS = kTokM ? 1 : C::kSB;  // scale tiles of 128 rows
+      auto weights = [&](int it) {
+        const int s = it % kS;
+        uint8_t* st = smem + s * (C::kABytes + C::kBBytes);
+        uint8_t* sc = scales + s * C::kScaleBytes;
+        mbar_expect_tx(&full[s], C::kStageBytes);
+        tma_load_2d(st + (kTokM ? C::kABytes : 0), &map_w, &full[s], (k0 + it) * KB, w_row);
+#pragma unroll
+        for (int i = 0; i < kWS; ++i)
+          bulk_load(sc + (kTokM ? 1 + i : 0) * 2 * kScaleTile,
+                    p.w_scale + ((w_row / 128 + i) * p.w_tiles + 2 * (k0 + it)) * kScaleTile,
+                    2 * kScaleTile, &full[s]);
+      };
+      auto tokens = [&](int it) {
+        const int s = it % kS;
+        uint8_t* st = smem + s * (C::kABytes + C::kBBytes);
+        uint8_t* sc = scales + s * C::kScaleBytes;
+        const int kc = group * p.groups_k + k0 + it;
+        tma_load_2d(st + (kTokM ? 0 : C::kABytes), &map_tok, &full[s], kc * KB, t0);
+#pragma unroll
+        for (int i = 0; i < kTS; ++i)
+          bulk_load(sc + (kTokM ? 0 : 1 + i) * 2 * kScaleTile,
+                    p.tok_scale + ((int64_t)(t0 / 128 + i) * p.tok_tiles + 2 * kc) * kScaleTile,
+                    2 * kScaleTile, &full[s]);
+      };
+      const int pre = nk < kS ? nk : kS;
+      for (int it = 0; it < pre; ++it) weights(it);
+      pdl_wait();
+      for (int it = 0; it < pre; ++it) tokens(it);
+      int it = pre;
+      for (; it < nk; ++it) {
+        if (!mbar_wait(&empty[it % kS], ((it / kS) & 1) ^ 1, p.status, abort_flag)) break;
+        weights(it);
+        tokens(it);
+      }
+      if (*abort_flag) {  // copies still in flight land before the CTA exits
+        for (int j = it - kS > 0 ? it - kS : 0; j < it; ++j)
+          mbar_wait(&full[j % kS], (j / kS) & 1, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer --
+    bool issued = false;
+    for (int it = 0; it < nk; ++it) {
+      const int s = it % C::kStages;
+      const bool ok = mbar_wait(&full[s], (it / C::kStages) & 1, p.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t ab = smem_u32(smem + s * (C::kABytes + C::kBBytes)), bb = ab + C::kABytes;
+        const uint32_t sc = smem_u32(scales + s * C::kScaleBytes);
+        // Scale columns of the stage: A's two tiles (4 columns each), then
+        // for each 128-value half of the chunk B's 4 or 8 columns.
+        const uint32_t ta = t_scale + s * C::kScaleCols, tb = ta + 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          copy_scales(ta + 4 * h, desc_scale(sc + h * kScaleTile));
+#pragma unroll
+          for (int i = 0; i < C::kSB; ++i)
+            copy_scales(tb + 4 * (C::kSB * h + i),
+                        desc_scale(sc + ((1 + i) * 2 + h) * kScaleTile));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_mxf4(tmem, desc_kmaj(ab + kk * 32), desc_kmaj(bb + kk * 32),
+                   idesc_mxf4(BM, BN, 2 * (kk & 1)), ta + 4 * (kk >> 1),
+                   tb + 4 * C::kSB * (kk >> 1), (it > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[s]);
+        if (it == nk - 1) mma_commit(accf);
+      }
+      __syncwarp();
+      issued = true;
+    }
+    if (*abort_flag && issued) {  // let issued MMAs finish before TMEM is freed
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, p.status);
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue --
+    const int q = warp & 3;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+    const bool ok = mbar_wait(accf, 0, p.status, abort_flag);
+    if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+      tc_fence_after();
+      if constexpr (!kTokM) {
+        // Lane = feature, columns = tokens: one coalesced store per token.
+        const int col = w_row + 32 * q + lane;
+        float* dst = p.part + (int64_t)split * p.T * p.ldc + col;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (t0 + c + j < p.T) dst[(int64_t)(t0 + c + j) * p.ldc] = __uint_as_float(v[j]);
+        }
+      } else {
+        // Lane = token, columns = features.
+        const int t = t0 + 32 * q + lane;
+        const bool live = t < p.T;
+        if (p.part) {
+          float* dst = p.part + ((int64_t)split * p.T + t) * p.ldc + w_row;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(acc + c, v);
+            tmem_wait_ld();
+            if (live) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4*>(dst + c + j) =
+                    make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            }
+          }
+        } else {
+          uint32_t sw = 0;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t v[32], w[16];
+            tmem_ld32(acc + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            if (live && p.c) {
+              uint4* dst = reinterpret_cast<uint4*>(p.c + (int64_t)t * p.ldc + w_row + c);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            }
+            if (p.yq) {  // one block: y as bf16 would hold it, quantised
+              uint32_t am = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                am = max(am, mx_amax8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j])));
+              const uint32_t sb = mx_scale_byte(am);
+              uint32_t cd[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                cd[j] = mx_quantise8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j]), sb);
+              sw |= sb << (8 * ((c >> 5) & 3));
+              if (live) {
+                const int k = w_row + c;  // y's column
+                *reinterpret_cast<uint4*>(p.yq + (int64_t)t * (p.ldc / 2) + k / 2) =
+                    make_uint4(cd[0], cd[1], cd[2], cd[3]);
+                if ((c & 96) == 96)
+                  *reinterpret_cast<uint32_t*>(
+                      p.ys + ((int64_t)(t / 128) * (p.ldc / 128) + k / 128) * kScaleTile +
+                      lane * 16 + q * 4) = sw;
+              }
+              if ((c & 96) == 96) sw = 0;
+            }
+          }
+        }
+      }
+    }
+  }
+  // Teardown: every warp reports (converged) that it is done with tensor
+  // memory; warp 0 frees it after all of them (bounded wait).
+  __syncwarp();
+  tc_fence_before();
+  if (lane == 0) mbar_arrive(done);
+  if (warp == 0) {
+    mbar_wait(done, 0, p.status);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Eight bf16 values of row t, columns 8*j .. +7 -> codes and, for every 16
+// lanes (128 columns), the word of their scale bytes.  All lanes take part.
+CSA_DEV void store_operand(uint8_t* codes, uint8_t* scales, int64_t cols, int64_t t, int64_t j,
+                           const uint32_t (&w)[4], bool live, int lane) {
+  uint32_t am = mx_amax8(w);
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  const uint32_t s = mx_scale_byte(am), cd = mx_quantise8(w, s);
+  uint32_t v = s << (8 * ((lane >> 2) & 3));
+  v |= __shfl_xor_sync(0xffffffffu, v, 4);
+  v |= __shfl_xor_sync(0xffffffffu, v, 8);
+  if (live) {
+    *reinterpret_cast<uint32_t*>(codes + t * (cols / 2) + 4 * j) = cd;
+    if ((lane & 15) == 0)
+      *reinterpret_cast<uint32_t*>(scales + ((t / 128) * (cols / 128) + j / 16) * kScaleTile +
+                                   (t % 32) * 16 + (t % 128) / 32 * 4) = v;
+  }
+}
+
+// Sum of the split partials [splits, T, cols] fp32, rounded to bf16: stored
+// (c) and, kQuant, quantised into the second product's operand.  Eight
+// columns per thread; cols is a multiple of 128.
+template <bool kQuant>
+__global__ void __launch_bounds__(256) mx_reduce_kernel(const float* __restrict__ part, int splits,
+                                                        int64_t n8, int64_t cols,
+                                                        __nv_bfloat16* __restrict__ c, uint8_t* yq,
+                                                        uint8_t* ys) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const bool live = i < n8;
+  pdl_trigger();
+  pdl_wait();  // the partials come from the GEMM kernel
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  if (live) {
+    const float* src = part + 8 * i;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(src + s * n8 * 8));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(src + s * n8 * 8) + 1);
+      x[0] += a.x;
+      x[1] += a.y;
+      x[2] += a.z;
+      x[3] += a.w;
+      x[4] += b.x;
+      x[5] += b.y;
+      x[6] += b.z;
+      x[7] += b.w;
+    }
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+  if (live && c) reinterpret_cast<uint4*>(c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (kQuant) {
+    const int64_t per = cols / 8;
+    store_operand(yq, ys, cols, i / per, i % per, w, live, threadIdx.x & 31);
+  }
+}
+
+// Rows of bf16 -> operand (codes and scale tiles).  blockIdx.x: 128 columns,
+// blockIdx.y: 128 rows; a warp reads two rows of 256 bytes at a time.  The
+// scale bytes of rows past the last one are written as zeros.
+__global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* __restrict__ x,
+                                                          int64_t ld_bytes, int64_t rows,
+                                                          int64_t cols, uint8_t* codes,
+                                                          uint8_t* scales) {
+  constexpr int kU = 8;  // rows of 16 threads each: 16 rows a step, 8 steps
+  __shared__ __align__(16) uint8_t sc[kScaleTile];
+  const int lane = threadIdx.x & 31, c = threadIdx.x & 15;
+  const int64_t r0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
+  const int rr = threadIdx.x >> 4;
+  const uint8_t* src = x + (r0 + rr) * ld_bytes + (k0 + 8 * c) * 2;
+  pdl_trigger();
+  uint4 v[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+    v[u] = r0 + rr + 16 * u < rows
+               ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)16 * u * ld_bytes))
+               : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    uint32_t am = mx_amax8(w);
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    const uint32_t s = mx_scale_byte(am), cd = mx_quantise8(w, s);
+    uint32_t b = s << (8 * ((lane >> 2) & 3));
+    b |= __shfl_xor_sync(0xffffffffu, b, 4);
+    b |= __shfl_xor_sync(0xffffffffu, b, 8);
+    const int r = rr + 16 * u;
+    if (r0 + r < rows)
+      *reinterpret_cast<uint32_t*>(codes + (r0 + r) * (cols / 2) + (k0 + 8 * c) / 2) = cd;
+    if (c == 0) *reinterpret_cast<uint32_t*>(sc + (r % 32) * 16 + r / 32 * 4) = b;
+  }
+  __syncthreads();
+  uint8_t* dst = scales + ((int64_t)blockIdx.y * (cols / 128) + blockIdx.x) * kScaleTile;
+  if (threadIdx.x < kScaleTile / 16)
+    reinterpret_cast<uint4*>(dst)[threadIdx.x] = reinterpret_cast<const uint4*>(sc)[threadIdx.x];
+}
+
+template <int BN, bool kTokM>
+cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
+  using C = Cfg<BN, kTokM>;
+  CUtensorMap map_tok, map_w;
+  cudaError_t e = make_tmap_2d(&map_tok, g.tok, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.T,
+                               (uint64_t)g.tok_k / 2, kTokM ? BM : BN, KB,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_2d(&map_w, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.groups * g.N,
+                   (uint64_t)g.K / 2, kTokM ? BN : BM, KB, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  GemmArgs p{};
+  p.tok_scale = static_cast<const uint8_t*>(g.tok_scale);
+  p.w_scale = static_cast<const uint8_t*>(g.w_scale);
+  p.T = g.T;
+  p.chunks = g.K / 256;
+  p.tok_tiles = g.tok_k / 128;
+  p.w_tiles = g.K / 128;
+  p.groups_k = p.chunks;
+  p.N = g.N;
+  p.splits = g.splits;
+  p.ldc = g.groups * g.N;
+  p.part = g.part;
+  p.c = static_cast<__nv_bfloat16*>(g.c);
+  p.yq = static_cast<uint8_t*>(g.yq);
+  p.ys = static_cast<uint8_t*>(g.ys);
+  p.status = g.status;
+  const size_t smem = 1024 + (size_t)C::kStages * C::kStageBytes + (2 * C::kStages + 3) * 8 + 16;
+  auto kern = mx_gemm_kernel<BN, kTokM>;
+  int slot = kTokM ? (BN == 256 ? 31 : 30) : 26;
+  if (!kTokM)
+    for (int b = 16; b < BN; b <<= 1) ++slot;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(kern), slot, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(g.N / (kTokM ? BN : BM), (g.T + (kTokM ? BM : BN) - 1) / (kTokM ? BM : BN),
+                  g.groups * g.splits);
+  e = launch_pdl(kern, grid, dim3(kThreads), smem, stream, 0, g.chained, map_tok, map_w, p);
+  if (e != cudaSuccess || !g.part) return e;
+  const int64_t n8 = (int64_t)g.T * p.ldc / 8;
+  const dim3 rgrid((unsigned)((n8 + 255) / 256));
+  if (g.yq)
+    return launch_pdl(mx_reduce_kernel<true>, rgrid, dim3(256), 0, stream, 0, 1,
+                      (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
+  return launch_pdl(mx_reduce_kernel<false>, rgrid, dim3(256), 0, stream, 0, 1,
+                    (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t cols, void* codes,
+                               void* scales, cudaStream_t stream) {
+  const dim3 grid((unsigned)(cols / 128), (unsigned)((rows + 127) / 128));
+  return launch_pdl(mx_quantise_kernel, grid, dim3(256), 0, stream, 0, 0,
+                    static_cast<const uint8_t*>(x), ld * 2, rows, cols,
+                    static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+}
+
+MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms) {
+  MxGemmPlan pl{};
+  const int chunks = K / 256;
+  if (T <= 128) {
+    pl.tok_m = 0;
+    pl.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  } else {
+    // Wide tiles when they still fill the SMs.
+    const int64_t wide = (int64_t)(N / 256) * groups * ((T + 127) / 128);
+    pl.tok_m = 1;
+    pl.bn = N % 256 == 0 && wide >= num_sms ? 256 : 128;
+  }
+  const int wt = pl.tok_m ? pl.bn : BM, tt = pl.tok_m ? BM : pl.bn;
+  const int64_t tiles = (int64_t)(N / wt) * groups * ((T + tt - 1) / tt);
+  const int64_t slots = (int64_t)num_sms * (pl.bn == 256 ? 1 : 2);
+  // K splits: as many as fit beside each other, at least four chunks each.
+  int64_t s = std::min<int64_t>(slots / std::max<int64_t>(1, tiles), chunks / 4);
+  pl.splits = (int)std::max<int64_t>(1, s);
+  pl.partials = !pl.tok_m || pl.splits > 1;
+  return pl;
+}
+
+cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t stream) {
+  if (g.T < 1 || g.N % 128 || g.K % 256 || g.splits < 1 || g.splits > g.K / 256 ||
+      (!g.tok_m && (g.T > g.bn || !g.part)) || (g.bn == 256 && g.N % 256))
+    return cudaErrorInvalidValue;
+  if ((g.T + 127) / 128 > 65535 || (int64_t)g.groups * g.splits > 65535)
+    return cudaErrorInvalidConfiguration;
+  if (g.tok_m) return g.bn == 256 ? launch_gemm<256, true>(g, stream) : launch_gemm<128, true>(g, stream);
+  switch (g.bn) {
+    case 16: return launch_gemm<16, false>(g, stream);
+    case 32: return launch_gemm<32, false>(g, stream);
+    case 64: return launch_gemm<64, false>(g, stream);
+    default: return launch_gemm<128, false>(g, stream);
+  }
+}
+
+}  // namespace csa

@@ -611,6 +611,49 @@ csa_status grouped_out_proj(int T, int H, int D, int g, int d_g, int d_model, co
                             size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The grouped output projection in MXFP4 (format: see the 4-bit cache above;
+ * the pages have no counterpart).  Weights are held in 4 bits; activations
+ * are quantised per token inside the call, in blocks of 32 along the inner
+ * dimension, as bf16 would hold them:
+ *   y[t, j*d_g + r] = bf16( sum_c W_g[j, r, c] * q(o)[t, j*(H/g)*D + c] )
+ *   z[t, n]         = bf16( sum_i W_o[n, i]    * q(y)[t, i] )
+ * with E2M1 products scaled per block and accumulated in fp32 on the tensor
+ * cores.  Other conventions as grouped_out_proj.
+ *
+ * Operand layout (weights, written once by mxfp4_quantize):
+ *   codes  [rows, cols/2] uint8: two codes a byte, the even column low
+ *   scales mxfp4_scale_bytes(rows, cols) = ceil(rows/128)*(cols/128)*512
+ *          bytes in tiles of 128 rows x 4 blocks, tile (r/128, c/128): the
+ *          scale of row r, columns 32*k .. +31 is byte
+ *          (r%32)*16 + (r%128)/32*4 + k%4 of tile (r/128, k/4); bytes of rows
+ *          past the last one are zero.
+ * mxfp4_quantize: x [rows, cols] bf16 (device), rows ld elements apart (a
+ * multiple of 8) -> codes, scales.  rows 0..8388480, cols a multiple of 128.
+ * A weight matrix with d_g or d_model rows is such an operand; W_g is one
+ * operand of g*d_g rows.
+ *
+ *   o [T, H, D] bf16; w_g [g*d_g, (H/g)*D/2], w_o [d_model, g*d_g/2] codes;
+ *   w_g_scale, w_o_scale scale tiles; y [T, g*d_g] bf16 (written: the values
+ *   before their quantisation) or NULL; z [T, d_model] bf16 (written).
+ * Supported: as grouped_out_proj with (H/g)*D and g*d_g multiples of 256,
+ * T <= 8388480.  A NaN or an infinity in a token's block makes that token's
+ * outputs NaN (in y: its group's; in z: all); other tokens are not affected.
+ * Workspace: grouped_out_proj_mxfp4_workspace_bytes (0 for unsupported
+ * arguments); CSA_ERR_WORKSPACE when smaller.
+ * ------------------------------------------------------------------------- */
+size_t mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+csa_status mxfp4_quantize(int64_t rows, int64_t cols, const void* x, int64_t ld, void* codes,
+                          void* scales, void* stream);
+
+size_t grouped_out_proj_mxfp4_workspace_bytes(int T, int H, int D, int g, int d_g, int d_model);
+
+csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_model, const void* o,
+                                  const void* w_g, const void* w_g_scale, const void* w_o,
+                                  const void* w_o_scale, void* y, void* z, void* ws,
+                                  size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Context split: one sequence's compressed cache over G devices.
  *
  * The pages give no parallel scheme for this path ("Architectural Overview

@@ -129,3 +129,43 @@ def test_binding_checks_shapes_before_the_library():
         binding.mxfp4_cache_read(p, kv4[:, :, :72], rows)
     with pytest.raises(TypeError):
         binding.mxfp4_cache_read(p, kv4, None)
+
+
+def test_scale_bytes_and_quantize_refusals(L):
+    assert L.mxfp4_scale_bytes(1, 128) == 512
+    assert L.mxfp4_scale_bytes(129, 256) == 2 * 2 * 512
+    for rows, cols in ((0, 128), (1, 96), (1, 0), (-1, 128), (65535 * 128 + 1, 128), (1, 1 << 25)):
+        assert L.mxfp4_scale_bytes(rows, cols) == 0, (rows, cols)
+
+    def call(rows=2, cols=256, x=None, ld=256, codes=None, scales=None):
+        return L.mxfp4_quantize(rows, cols, x, ld, codes, scales, None)
+    assert call(rows=0) == 0
+    assert call(rows=-1) == 2
+    assert call(cols=200) == 2
+    assert call(ld=128) == 1
+    assert call(ld=260) == 1
+    assert call() == 1 and b"x is null" in L.csa_last_error()
+    assert call(x=8) == 1
+    assert call(x=16) == 1 and b"codes is null" in L.csa_last_error()
+    assert call(x=16, codes=16) == 1 and b"scales is null" in L.csa_last_error()
+
+
+def test_projection_refusals(L):
+    ok = (8, 16, 128, 4, 128, 256)
+    assert L.grouped_out_proj_mxfp4_workspace_bytes(*ok) > 0
+    bad = [((0, 16, 128, 4, 128, 256), 1), ((8, 16, 128, 3, 128, 256), 2),
+           ((8, 16, 128, 4, 64, 256), 2), ((8, 16, 128, 4, 128, 200), 2),
+           ((8, 1, 128, 1, 256, 256), 2),         # (H/g)*D = 128
+           ((8, 16, 128, 1, 128, 256), 2),        # g*d_g = 128
+           ((65535 * 128 + 1, 16, 128, 4, 128, 256), 2)]
+    null = (None,) * 8 + (0, None, None)
+    for sizes, code in bad:
+        assert L.grouped_out_proj_mxfp4_workspace_bytes(*sizes) == 0, sizes
+        assert L.grouped_out_proj_mxfp4(*sizes, *null) == code, sizes
+    assert L.grouped_out_proj_mxfp4(*ok, *null) == 1 and b"o is null" in L.csa_last_error()
+    p = (16, 16, 16, 16, 16, None, 16)
+    assert L.grouped_out_proj_mxfp4(*ok, *p, None, 0, None, None) == 4   # no workspace
+    assert L.grouped_out_proj_mxfp4(*ok, *p, 16, 100, None, None) == 4   # too small
+    assert L.grouped_out_proj_mxfp4(*ok, *p, 8, 1 << 40, None, None) == 1  # misaligned
+    with pytest.raises(ValueError):
+        binding.grouped_out_proj_mxfp4(torch.zeros(2, 3), None, None, None, None, None)
