@@ -168,6 +168,12 @@ struct MxTile {
   }
 };
 
+// A pair of the MMA's 16-bit operands.
+template <bool kF16>
+CSA_DEV uint32_t pack16(float lo, float hi) {
+  return kF16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+
 CSA_DEV uint64_t desc_k(uint32_t saddr) { return sdesc_sw128(saddr, 16, 1024); }
 CSA_DEV uint64_t desc_mn(uint32_t saddr) { return sdesc_sw128(saddr, TN * 128, 1024); }
 
@@ -572,8 +578,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer --
     constexpr int kPvN = D >= 256 ? 256 : D;  // N of one P.V instruction
-    const uint32_t idesc_s = idesc_bf16(64, TN, 0, 0);
-    const uint32_t idesc_pv = idesc_bf16(64, kPvN, 0, 1);
+    const uint32_t idesc_s = kMx ? idesc_f16(64, TN, 0, 0) : idesc_bf16(64, TN, 0, 0);
+    const uint32_t idesc_pv = kMx ? idesc_f16(64, kPvN, 0, 1) : idesc_bf16(64, kPvN, 0, 1);
     const bool ok = wait_all(qready, 0, p, abort_flag);
     tc_fence_after();
     bool issued = false;
@@ -672,17 +678,84 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       }
       return true;
     };
+    // Window tokens of an MXFP4 call, four threads a row: raw bf16 rows ->
+    // normalised, rotated, rounded once to fp16 (in place: a thread reads and
+    // writes the same 16-byte units).
+    auto window_f16 = [&](const Meta& M, uint8_t* st) {
+      const int wr = tid >> 2, hq = tid & 3;
+      const bool valid = (M.valid[wr >> 5] >> (wr & 31)) & 1u;
+      constexpr int kPlain = (D - R) / 8;  // units without rotation
+      float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int c = hq; c < D / 8; c += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(st + tile_off(wr, c * 8));
+        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = bf16_lo(w4[e]), hi = bf16_hi(w4[e]);
+          a4[e] = fmaf(lo, lo, fmaf(hi, hi, a4[e]));
+        }
+      }
+      float ss = (a4[0] + a4[1]) + (a4[2] + a4[3]);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+      const float rn = 1.0f / sqrtf(ss / (float)D + p.eps);
+      __syncwarp();  // every unit of the row is read before one is rewritten
+#pragma unroll 2
+      for (int c = hq; c < kPlain; c += 4) {
+        uint4* at = reinterpret_cast<uint4*>(st + tile_off(wr, c * 8));
+        const uint4 u = *at;
+        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+        const float* g = gam_s + D + c * 8;
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = valid ? pack_f16(bf16_lo(w4[e]) * rn * g[2 * e], bf16_hi(w4[e]) * rn * g[2 * e + 1])
+                       : 0u;  // masked rows enter P.V with P = 0: finite zeros
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if constexpr (R > 0) {
+        // Pairs (j, j + R/2) of the last R dims, eight of them per thread.
+        constexpr int half = R / 2, d0 = D - R;
+        if (hq < R / 16) {
+          const int j0 = 8 * hq;
+          const double ppos = (double)M.pos[wr];
+          uint4* pa = reinterpret_cast<uint4*>(st + tile_off(wr, d0 + j0));
+          uint4* pb = reinterpret_cast<uint4*>(st + tile_off(wr, d0 + half + j0));
+          const uint4 ua = *pa, ub = *pb;
+          const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
+          const float* g = gam_s + D + d0 + j0;
+          uint32_t oa[4], ob[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float s0, c0, s1, c1;
+            sincos_reduced(ppos * p.inv_freq[j0 + 2 * e], &s0, &c0);
+            sincos_reduced(ppos * p.inv_freq[j0 + 2 * e + 1], &s1, &c1);
+            const float x10 = bf16_lo(wa[e]) * rn * g[2 * e];
+            const float x11 = bf16_hi(wa[e]) * rn * g[2 * e + 1];
+            const float x20 = bf16_lo(wb[e]) * rn * g[half + 2 * e];
+            const float x21 = bf16_hi(wb[e]) * rn * g[half + 2 * e + 1];
+            oa[e] = valid ? pack_f16(x10 * c0 - x20 * s0, x11 * c1 - x21 * s1) : 0u;
+            ob[e] = valid ? pack_f16(x20 * c0 + x10 * s0, x21 * c1 + x11 * s1) : 0u;
+          }
+          *pa = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+          *pb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+      }
+    };
     // One tile whose rows land in the stage as bf16: wait for them, zero the
     // masked ones, normalise and rotate window tokens, hand the tile over.
     auto transform = [&](int it) -> bool {
       const int s = it % C::kStages;
       if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) return false;
-      if (tid >= 128) {  // two threads a row here: the other warps pass
+      Meta& M = meta[s];
+      uint8_t* st = stages + s * C::kStageBytes;
+      if constexpr (kMx) {
+        window_f16(M, st);
+        fence_proxy_async_smem();
         mbar_arrive(&ready[s]);
         return true;
       }
-      Meta& M = meta[s];
-      uint8_t* st = stages + s * C::kStageBytes;
       const bool valid = (M.valid[r >> 5] >> (r & 31)) & 1u;
       if (!valid) {  // masked rows enter P.V with P = 0: make them finite zeros
         for (int c = hf; c < D / 8; c += 2)
@@ -750,7 +823,12 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     if constexpr (kMx) {
       // MXFP4 entries: a thread holds whole blocks of 32 values (16 bytes of
       // codes and their scale byte), fetched one tile ahead straight into
-      // registers; their bf16 values (exact) go into the stage.  64 rows are
+      // registers; their fp16 values go into the stage (exact from scale
+      // 2^-23 on).  Every operand of these products is fp16 (queries,
+      // weights P and window tokens too), not bf16: its three more bits take
+      // the error against 64 bits from 2.7e-3 .. 3.4e-3 (relative, L2) to the
+      // 1.7e-3 that rounding the output to bf16 alone costs, in the same
+      // time, and normalised rows fit its range.  64 rows are
       // 17 KB against 64 KB of bf16.  The conversion takes about five
       // instructions a pair of values; its loop stays rolled (one block a
       // turn, the registers shifted down), since the unrolled one waited on
@@ -808,15 +886,18 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
 #pragma unroll 1
             for (int u = 0; u < X::kU; ++u) {
               const uint32_t w[4] = {cd[0].x, cd[0].y, cd[0].z, cd[0].w};
-              const MxScale scale(sc[0]);
+              const uint32_t lo = mx_f16_lo(sc[0]);
               const bool wide = __any_sync(0xffffffffu, sc[0] > 128u);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t o[4];
-                mx_values8(w[j], scale.lo, o);
+                mx_values8_f16(w[j], lo, o);
                 if (wide) {
+                  const uint32_t hi = mx_f16_hi(sc[0]);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], scale.hi);
+                  for (int i = 0; i < 4; ++i) o[i] = mul_f16x2(o[i], hi);
+                  if (sc[0] > kMxF16Top && sc[0] != 255u)
+                    report(p.status, CSA_ERR_UNSUPPORTED_SHAPE);
                 }
                 *reinterpret_cast<uint4*>(unit[j]) = make_uint4(o[0], o[1], o[2], o[3]);
                 unit[j] += X::kStep * 128;
@@ -954,7 +1035,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         }
         uint32_t pk[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        for (int e = 0; e < 32; ++e) pk[e] = pack16<kMx>(x[2 * e], x[2 * e + 1]);
         tmem_st_16x32bx2_x32<D / 4>(t_q + lq + 32 * c, pk);
       }
       tmem_wait_st();
@@ -979,7 +1060,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       }
       if (!wait_all(&ready[s], (it / C::kStages) & 1, p, abort_flag)) break;
       const Meta& M = meta[s];
-      const bool win = M.window != 0;
+      const bool win = !kMx && M.window != 0;  // (kMx: normalised in the stage)
       const uint32_t vw = M.valid[hf];
       // Logits (log2 domain); window columns times 1/rms(c_t).  Entry tiles
       // without a masked row (most tiles of a long list) take packed
@@ -1057,8 +1138,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
           const float2 pb = make_float2(fast_exp2(xb.x), fast_exp2(xb.y));
           la = add_f32x2(la, pa);
           lb = add_f32x2(lb, pb);
-          pk[j / 2] = pack_bf16(pa.x, pa.y);
-          pk[j / 2 + 1] = pack_bf16(pb.x, pb.y);
+          pk[j / 2] = pack16<kMx>(pa.x, pa.y);
+          pk[j / 2 + 1] = pack16<kMx>(pb.x, pb.y);
         }
         l4[0] = la.x;
         l4[1] = la.y;
@@ -1075,7 +1156,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
             p0 *= M.rn[32 * hf + j];
             p1 *= M.rn[32 * hf + j + 1];
           }
-          pk[j / 2] = pack_bf16(p0, p1);
+          pk[j / 2] = pack16<kMx>(p0, p1);
         }
       }
       float ls = (l4[0] + l4[1]) + (l4[2] + l4[3]);

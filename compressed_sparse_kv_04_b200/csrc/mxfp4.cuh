@@ -102,4 +102,32 @@ CSA_DEV void mx_values8(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
   }
 }
 
+// The same in fp16, the form the attention's tensor cores take: a code's
+// exponent and mantissa bits at bits 11..9 of an fp16 are its magnitude times
+// 2^-14, so the factor is 2^(s-113): one product for s <= 128 (scales below
+// 2^-24 / 2^-14 vanish), a second factor 2^(s-128) up to s = 140 (values up
+// to 49152).  Above that (and for 255) the values are NaN.
+constexpr uint32_t kMxF16Top = 140u;
+CSA_DEV uint32_t mx_f16_lo(uint32_t s) {
+  const float f = __uint_as_float((min(s, 128u) + 14u) << 23);  // 2^(min(s, 128) - 113)
+  return h2_bits(__floats2half2_rn(f, f));
+}
+CSA_DEV uint32_t mx_f16_hi(uint32_t s) {
+  return (s > kMxF16Top ? 0x7E00u : (max(s, 128u) - 113u) << 10) * 0x10001u;
+}
+CSA_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+CSA_DEV void mx_values8_f16(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
+  const uint32_t v = w << 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t sel = (uint32_t)(i | (i << 4) | ((i + 4) << 8) | ((i + 4) << 12));
+    const uint32_t r = __byte_perm(v, w, sel);
+    o[i] = mul_f16x2((r & 0x80008000u) | ((r >> 3) & 0x0E000E00u), lo);
+  }
+}
+
 }  // namespace csa

@@ -511,10 +511,15 @@ csa_status mxfp4_cache_read(const csa_params* p, const void* kv4, int64_t N_cap,
  * without the suffix, with kv4 in place of kv_c.
  *   - Writing calls quantise each entry as the bf16 cache would hold it: the
  *     bytes are those of mxfp4_cache_write on the bf16 entry.
- *   - Attending calls use each entry's stored values (exact in bf16); window
- *     tokens stay bf16.  An entry that reads back as NaN and is selected (or
- *     visible, dense) makes its rows NaN; entries that are not selected are
- *     never read.
+ *   - Attending calls use each entry's stored values; window tokens stay
+ *     bf16.  The products take fp16 operands (query, entries, window rows and
+ *     weights each rounded once, to 11 bits, where the calls on bf16 caches
+ *     round to 8), which normalised rows fit: entries with a scale byte of
+ *     104 .. 140 (2^-23 .. 2^13) are exact, smaller ones round to multiples
+ *     of 2^-24, and a larger one is reported (CSA_ERR_UNSUPPORTED_SHAPE in
+ *     dev_status) and counts as NaN.  Gains up to 2048 in magnitude fit.
+ *   - An entry that is NaN and is selected (or visible, dense) makes its
+ *     row's outputs NaN; entries that are not selected are never read.
  *   - The indexer's keys are the E4M3 keys of the bf16 cache.
  * The context split below takes bf16 caches only. */
 csa_status hca_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,
