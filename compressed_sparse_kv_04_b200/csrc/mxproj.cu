@@ -22,15 +22,18 @@
 // the MMAs that read its former scales have completed (its `full` barrier
 // follows its `empty` barrier).
 //
-// Two forms of one kernel:
+// Two forms of one kernel (mx_gemm_kernel):
 //   - few tokens (T <= 128): weights are the MMA's M = 128 rows, tokens its N.
 //     The weights' bytes bound it: K is split so that two CTAs on every SM
 //     stream them; fp32 partials are summed by the kernel that quantises y
 //     (or stores z).
-//   - more tokens: tokens are the M = 128 rows, weights N = 128 or 256, so
-//     that a thread of the epilogue holds one token's neighbouring features
-//     and quantises y in registers.
+//   - more tokens: tokens are the M = 128 rows, weights N = 128, so that a
+//     thread of the epilogue holds one token's neighbouring features and
+//     quantises y in registers; K is split where the tiles do not fill the
+//     SMs (then y is quantised by the kernel that sums the partials).
+// and a second kernel on CTA pairs for many tokens (mx_pair_kernel).
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.h"
 #include "mxfp4.cuh"
@@ -98,20 +101,51 @@ struct GemmArgs {
   int32_t* status;
 };
 
+// One 32-value block of a token's row (fp32 in v): bf16 into c, and quantised
+// into the next product's operand (yq, and its scale byte returned).
+CSA_DEV uint32_t store_block(const GemmArgs& p, int t, int k, const uint32_t* v, bool live) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+  if (live && p.c) {
+    uint4* dst = reinterpret_cast<uint4*>(p.c + (int64_t)t * p.ldc + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+  if (!p.yq) return 0;
+  uint32_t am = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    am = max(am, mx_amax8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j])));
+  const uint32_t sb = mx_scale_byte(am);
+  uint32_t cd[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    cd[j] = mx_quantise8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j]), sb);
+  if (live)
+    *reinterpret_cast<uint4*>(p.yq + (int64_t)t * (p.ldc / 2) + k / 2) =
+        make_uint4(cd[0], cd[1], cd[2], cd[3]);
+  return sb;
+}
+// The four scale bytes of columns k .. k + 127 (k a multiple of 128).
+CSA_DEV void store_scales(const GemmArgs& p, int t, int k, uint32_t word) {
+  *reinterpret_cast<uint32_t*>(p.ys + ((int64_t)(t / 128) * (p.ldc / 128) + k / 128) * kScaleTile +
+                               (t % 32) * 16 + (t % 128) / 32 * 4) = word;
+}
+
 template <int BN, bool kTokM>
 struct Cfg {
-  static constexpr int kSB = BN > 128 ? 2 : 1;             // 128-row scale tiles of B
   static constexpr int kABytes = BM * KB;
   static constexpr int kBBytes = BN * KB;
-  static constexpr int kScaleBytes = (1 + kSB) * 2 * kScaleTile;
+  static constexpr int kScaleBytes = 4 * kScaleTile;       // two tiles of A, two of B
   static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
-  // One CTA per SM at BN = 256, else two.
-  static constexpr int kCtas = BN > 128 ? 1 : 2;
-  static constexpr int kStages = (kCtas == 1 ? 208 : 103) * 1024 / kStageBytes;
-  static constexpr int kScaleCols = (1 + kSB) * 8;         // columns of a stage's scales
+  static constexpr int kStages = 103 * 1024 / kStageBytes; // two CTAs per SM
+  static constexpr int kScaleCols = 16;                    // columns of a stage's scales
   static constexpr int kCols0 = (BN < 32 ? 32 : BN) + kStages * kScaleCols;
-  static constexpr uint32_t kCols = kCols0 <= 128 ? 128 : (kCols0 <= 256 ? 256 : 512);
-  static_assert(kStages >= 2 && kCols0 <= 512 && kCtas * (int)kCols <= 512, "tensor memory");
+  static constexpr uint32_t kCols = kCols0 <= 128 ? 128 : 256;
+  static_assert(BN <= 128 && kStages >= 2 && kCols0 <= 256, "tensor memory of two CTAs");
 };
 
 template <int BN, bool kTokM>
@@ -173,18 +207,15 @@ __global__ void __launch_bounds__(kThreads)
       tma_prefetch_desc(&map_tok);
       tma_prefetch_desc(&map_w);
       constexpr int kS = C::kStages;
-      constexpr int kWS = kTokM ? C::kSB : 1, kTS = kTokM ? 1 : C::kSB;  // scale tiles of 128 rows
       auto weights = [&](int it) {
         const int s = it % kS;
         uint8_t* st = smem + s * (C::kABytes + C::kBBytes);
         uint8_t* sc = scales + s * C::kScaleBytes;
         mbar_expect_tx(&full[s], C::kStageBytes);
         tma_load_2d(st + (kTokM ? C::kABytes : 0), &map_w, &full[s], (k0 + it) * KB, w_row);
-#pragma unroll
-        for (int i = 0; i < kWS; ++i)
-          bulk_load(sc + (kTokM ? 1 + i : 0) * 2 * kScaleTile,
-                    p.w_scale + ((w_row / 128 + i) * p.w_tiles + 2 * (k0 + it)) * kScaleTile,
-                    2 * kScaleTile, &full[s]);
+        bulk_load(sc + (kTokM ? 2 * kScaleTile : 0),
+                  p.w_scale + (w_row / 128 * p.w_tiles + 2 * (k0 + it)) * kScaleTile,
+                  2 * kScaleTile, &full[s]);
       };
       auto tokens = [&](int it) {
         const int s = it % kS;
@@ -192,11 +223,9 @@ __global__ void __launch_bounds__(kThreads)
         uint8_t* sc = scales + s * C::kScaleBytes;
         const int kc = group * p.groups_k + k0 + it;
         tma_load_2d(st + (kTokM ? 0 : C::kABytes), &map_tok, &full[s], kc * KB, t0);
-#pragma unroll
-        for (int i = 0; i < kTS; ++i)
-          bulk_load(sc + (kTokM ? 0 : 1 + i) * 2 * kScaleTile,
-                    p.tok_scale + ((int64_t)(t0 / 128 + i) * p.tok_tiles + 2 * kc) * kScaleTile,
-                    2 * kScaleTile, &full[s]);
+        bulk_load(sc + (kTokM ? 0 : 2 * kScaleTile),
+                  p.tok_scale + (t0 / 128 * p.tok_tiles + 2 * kc) * kScaleTile, 2 * kScaleTile,
+                  &full[s]);
       };
       const int pre = nk < kS ? nk : kS;
       for (int it = 0; it < pre; ++it) weights(it);
@@ -225,22 +254,18 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) {
         const uint32_t ab = smem_u32(smem + s * (C::kABytes + C::kBBytes)), bb = ab + C::kABytes;
         const uint32_t sc = smem_u32(scales + s * C::kScaleBytes);
-        // Scale columns of the stage: A's two tiles (4 columns each), then
-        // for each 128-value half of the chunk B's 4 or 8 columns.
+        // Scale columns of the stage: A's two tiles, then B's (4 columns each).
         const uint32_t ta = t_scale + s * C::kScaleCols, tb = ta + 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           copy_scales(ta + 4 * h, desc_scale(sc + h * kScaleTile));
-#pragma unroll
-          for (int i = 0; i < C::kSB; ++i)
-            copy_scales(tb + 4 * (C::kSB * h + i),
-                        desc_scale(sc + ((1 + i) * 2 + h) * kScaleTile));
+          copy_scales(tb + 4 * h, desc_scale(sc + (2 + h) * kScaleTile));
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_mxf4(tmem, desc_kmaj(ab + kk * 32), desc_kmaj(bb + kk * 32),
                    idesc_mxf4(BM, BN, 2 * (kk & 1)), ta + 4 * (kk >> 1),
-                   tb + 4 * C::kSB * (kk >> 1), (it > 0 || kk > 0) ? 1u : 0u);
+                   tb + 4 * (kk >> 1), (it > 0 || kk > 0) ? 1u : 0u);
         mma_commit(&empty[s]);
         if (it == nk - 1) mma_commit(accf);
       }
@@ -294,39 +319,13 @@ __global__ void __launch_bounds__(kThreads)
           uint32_t sw = 0;
 #pragma unroll 1
           for (int c = 0; c < BN; c += 32) {
-            uint32_t v[32], w[16];
+            uint32_t v[32];
             tmem_ld32(acc + c, v);
             tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            if (live && p.c) {
-              uint4* dst = reinterpret_cast<uint4*>(p.c + (int64_t)t * p.ldc + w_row + c);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            }
-            if (p.yq) {  // one block: y as bf16 would hold it, quantised
-              uint32_t am = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                am = max(am, mx_amax8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j])));
-              const uint32_t sb = mx_scale_byte(am);
-              uint32_t cd[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                cd[j] = mx_quantise8(*reinterpret_cast<const uint32_t(*)[4]>(&w[4 * j]), sb);
-              sw |= sb << (8 * ((c >> 5) & 3));
-              if (live) {
-                const int k = w_row + c;  // y's column
-                *reinterpret_cast<uint4*>(p.yq + (int64_t)t * (p.ldc / 2) + k / 2) =
-                    make_uint4(cd[0], cd[1], cd[2], cd[3]);
-                if ((c & 96) == 96)
-                  *reinterpret_cast<uint32_t*>(
-                      p.ys + ((int64_t)(t / 128) * (p.ldc / 128) + k / 128) * kScaleTile +
-                      lane * 16 + q * 4) = sw;
-              }
-              if ((c & 96) == 96) sw = 0;
+            sw |= store_block(p, t, w_row + c, v, live) << (c & 96) / 4;
+            if ((c & 96) == 96) {
+              if (live && p.yq) store_scales(p, t, w_row + c - 96, sw);
+              sw = 0;
             }
           }
         }
@@ -344,6 +343,244 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
+}
+
+// ------------------------------------------------------------- CTA pairs --
+// Many tokens: tiles of 256 tokens x 256 features on pairs of CTAs
+// (cta_group::2).  Each CTA loads its 128 tokens and half of the weight rows,
+// so a chunk costs an SM 35 KB from L2 for 128 x 256 x 256 products (48 KB
+// where each CTA loads a whole 256-row weight tile: that form was bound by L2
+// at 12 TB/s).  The grid is persistent (one CTA per SM); the epilogue's eight
+// warps take the accumulator into registers at once, so the next tile's MMAs
+// start while they convert and store it.
+constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
+struct Pair {
+  static constexpr int kStages = 6;
+  static constexpr int kOperand = BM * KB;            // 128 token rows, or 128 weight rows
+  static constexpr int kScaleBytes = 6 * kScaleTile;  // the tokens' tiles, all weight rows'
+  static constexpr int kStageBytes = 2 * kOperand + kScaleBytes;
+  static constexpr int kScaleCols = 24;               // A 2 x 4, B 2 x 8 columns
+  static constexpr int kAccCols = 256;
+  static constexpr uint32_t kCols = 512;
+  static_assert(kAccCols + kStages * kScaleCols <= 512, "tensor memory");
+};
+
+CSA_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                              int32_t y) {
+  // The bytes count on the even CTA's barrier (bit 24 of the cluster shared
+  // address tells the CTAs of a pair apart).
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(x), "r"(y)
+      : "memory");
+}
+CSA_DEV void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                           uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;"
+      "\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+      : "memory");
+}
+CSA_DEV void copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+// Arrive on `bar` of both CTAs when the pair's earlier MMAs have completed.
+CSA_DEV void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap map_tok,
+                   const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_ts,
+                   const __grid_constant__ CUtensorMap map_ws, const GemmArgs p) {
+  using C = Pair;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* scales = smem + C::kStages * 2 * C::kOperand;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kStages * C::kScaleBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* accf = empty + C::kStages;  // a tile's accumulator is complete
+  uint64_t* acce = accf + 1;            // (even CTA) both CTAs have read it
+  uint64_t* drain = acce + 1;           // issued MMAs finished (abort path)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = (int)cluster_ctarank();
+  const int m_tiles = (p.T + 255) / 256, n_group = p.N / 256;
+  const int tiles = m_tiles * (p.ldc / 256);
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(acce, 16);  // eight epilogue warps of either CTA
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers and tensor memory are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer --
+    if (elect_one()) {
+      tma_prefetch_desc(&map_tok);
+      tma_prefetch_desc(&map_w);
+      tma_prefetch_desc(&map_ts);
+      tma_prefetch_desc(&map_ws);
+      pdl_wait();
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < tiles; tile += step) {
+        const int m = tile % m_tiles, n = tile / m_tiles;
+        const int kg = n / n_group * p.chunks;  // the group's first token chunk
+        for (int c = 0; c < p.chunks; ++c, ++it) {
+          const int s = it % C::kStages;
+          if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * 2 * C::kOperand;
+          uint8_t* sc = scales + s * C::kScaleBytes;
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStageBytes);
+          tma_load_2d_pair(st, &map_tok, &full[s], (kg + c) * KB, m * 256 + rank * 128);
+          tma_load_2d_pair(st + C::kOperand, &map_w, &full[s], c * KB, n * 256 + rank * 128);
+          // (Scale tiles past the last token lie past the map: zeros.)
+          tma_load_2d_pair(sc, &map_ts, &full[s], 0,
+                           (int32_t)((2 * m + rank) * p.tok_tiles) + 2 * (kg + c));
+          tma_load_2d_pair(sc + 2 * kScaleTile, &map_ws, &full[s], 0,
+                           (int32_t)(2 * n * p.w_tiles) + 2 * c);
+          tma_load_2d_pair(sc + 4 * kScaleTile, &map_ws, &full[s], 0,
+                           (int32_t)((2 * n + 1) * p.w_tiles) + 2 * c);
+        }
+      }
+      if (*abort_flag) {  // copies still in flight land before the CTA exits
+        if (rank == 0)
+          for (int j = it - C::kStages > 0 ? it - C::kStages : 0; j < it; ++j)
+            mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, p.status);
+        // (The odd CTA's copies count on the even CTA's barriers: wait out
+        // their latency.)
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer --
+    if (rank == 0) {
+      const uint32_t t_scale = tmem + C::kAccCols;
+      bool issued = false, ok = true;
+      int it = 0, j = 0;
+      for (int tile = first; ok && tile < tiles; tile += step, ++j) {
+        if (j > 0) {
+          ok = mbar_wait<true>(acce, (j - 1) & 1, p.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+        }
+        for (int c = 0; ok && c < p.chunks; ++c, ++it) {
+          const int s = it % C::kStages;
+          ok = mbar_wait<true>(&full[s], (it / C::kStages) & 1, p.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ab = smem_u32(smem + s * 2 * C::kOperand), bb = ab + C::kOperand;
+            const uint32_t sc = smem_u32(scales + s * C::kScaleBytes);
+            const uint32_t ta = t_scale + s * C::kScaleCols, tb = ta + 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              copy_scales_pair(ta + 4 * h, desc_scale(sc + h * kScaleTile));
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                copy_scales_pair(tb + 8 * h + 4 * i,
+                                 desc_scale(sc + ((1 + i) * 2 + h) * kScaleTile));
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_mxf4_pair(tmem, desc_kmaj(ab + kk * 32), desc_kmaj(bb + kk * 32),
+                            idesc_mxf4(256, 256, 2 * (kk & 1)), ta + 4 * (kk >> 1),
+                            tb + 8 * (kk >> 1), (c > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&empty[s]);
+            if (c == p.chunks - 1) mma_commit_pair(accf);
+          }
+          __syncwarp();
+          issued = true;
+        }
+      }
+      if (*abort_flag && issued) {  // let issued MMAs finish before TMEM is freed
+        if (elect_one())
+          asm volatile(
+              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                  smem_u32(drain))
+              : "memory");
+        __syncwarp();
+        mbar_wait(drain, 0, p.status);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue --
+    // Two warps per lane quarter, 128 columns each; lane = token.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
+    const uint32_t acce0 = mapa(smem_u32(acce), 0);
+    int j = 0;
+    for (int tile = first; tile < tiles; tile += step, ++j) {
+      const bool ok = mbar_wait<true>(accf, j & 1, p.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(acc + 32 * c, v[c]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(acce0);
+      const int t = tile % m_tiles * 256 + rank * 128 + 32 * q + lane;
+      const int k = tile / m_tiles * 256 + 128 * half;
+      const bool live = t < p.T;
+      uint32_t sw = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sw |= store_block(p, t, k + 32 * c, v[c], live) << (8 * c);
+      if (live && p.yq) store_scales(p, t, k, sw);
+    }
+  }
+  // Every wait above is bounded, so every thread of both CTAs arrives here;
+  // after it nothing of the pair reads the other's memory.
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols)
+                 : "memory");
 }
 
 // Eight bf16 values of row t, columns 8*j .. +7 -> codes and, for every 16
@@ -476,7 +713,7 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
   p.status = g.status;
   const size_t smem = 1024 + (size_t)C::kStages * C::kStageBytes + (2 * C::kStages + 3) * 8 + 16;
   auto kern = mx_gemm_kernel<BN, kTokM>;
-  int slot = kTokM ? (BN == 256 ? 31 : 30) : 26;
+  int slot = kTokM ? 30 : 26;
   if (!kTokM)
     for (int b = 16; b < BN; b <<= 1) ++slot;
   e = ensure_smem_attr(reinterpret_cast<const void*>(kern), slot, smem);
@@ -492,6 +729,73 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
                       (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
   return launch_pdl(mx_reduce_kernel<false>, rgrid, dim3(256), 0, stream, 0, 1,
                     (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
+}
+
+// Pairs of CTAs that can be resident at once on this device (one persistent
+// pair each).
+int pairs_resident(size_t smem) {
+  static std::atomic<int> cached[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return std::max(1, device_sm_count() / 2);
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // a refused query is not the caller's error
+      n = std::max(1, device_sm_count() / 2);
+    }
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+cudaError_t launch_pair(const MxGemm& g, cudaStream_t stream) {
+  using C = Pair;
+  CUtensorMap map_tok, map_w, map_ts, map_ws;
+  cudaError_t e = make_tmap_2d(&map_tok, g.tok, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.T,
+                               (uint64_t)g.tok_k / 2, BM, KB, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_2d(&map_w, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.groups * g.N,
+                   (uint64_t)g.K / 2, BM, KB, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  // Scale tiles as rows of 128 words, two neighbouring tiles a load.
+  const uint64_t t_rows = (uint64_t)(g.T + 127) / 128 * (g.tok_k / 128);
+  const uint64_t w_rows = (uint64_t)g.groups * g.N / 128 * (g.K / 128);
+  e = make_tmap_2d(&map_ts, g.tok_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, t_rows,
+                   kScaleTile / 4, 2, kScaleTile / 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_2d(&map_ws, g.w_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w_rows, kScaleTile / 4,
+                   2, kScaleTile / 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (e != cudaSuccess) return e;
+  GemmArgs p{};
+  p.T = g.T;
+  p.chunks = g.K / 256;
+  p.tok_tiles = g.tok_k / 128;
+  p.w_tiles = g.K / 128;
+  p.N = g.N;
+  p.ldc = g.groups * g.N;
+  p.c = static_cast<__nv_bfloat16*>(g.c);
+  p.yq = static_cast<uint8_t*>(g.yq);
+  p.ys = static_cast<uint8_t*>(g.ys);
+  p.status = g.status;
+  const size_t smem = 1024 + (size_t)C::kStages * C::kStageBytes + (2 * C::kStages + 3) * 8 + 16;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(mx_pair_kernel), 31, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)((g.T + 255) / 256) * (p.ldc / 256);
+  const int pairs = (int)std::min<int64_t>(tiles, pairs_resident(smem));
+  return launch_pdl(mx_pair_kernel, dim3(2 * pairs), dim3(kPairThreads), smem, stream, 2, g.chained,
+                    map_tok, map_w, map_ts, map_ws, p);
 }
 
 }  // namespace
@@ -511,14 +815,18 @@ MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms) {
     pl.tok_m = 0;
     pl.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
   } else {
-    // Wide tiles when they still fill the SMs.
-    const int64_t wide = (int64_t)(N / 256) * groups * ((T + 127) / 128);
+    // CTA pairs where their tiles (256 x 256) give every pair of SMs one.
+    const int64_t wide = (int64_t)(N / 256) * groups * ((T + 255) / 256);
     pl.tok_m = 1;
-    pl.bn = N % 256 == 0 && wide >= num_sms ? 256 : 128;
+    pl.bn = N % 256 == 0 && wide >= num_sms / 2 ? 256 : 128;
+    if (pl.bn == 256) {
+      pl.splits = 1;
+      return pl;
+    }
   }
   const int wt = pl.tok_m ? pl.bn : BM, tt = pl.tok_m ? BM : pl.bn;
   const int64_t tiles = (int64_t)(N / wt) * groups * ((T + tt - 1) / tt);
-  const int64_t slots = (int64_t)num_sms * (pl.bn == 256 ? 1 : 2);
+  const int64_t slots = (int64_t)num_sms * 2;
   // K splits: as many as fit beside each other, at least four chunks each.
   int64_t s = std::min<int64_t>(slots / std::max<int64_t>(1, tiles), chunks / 4);
   pl.splits = (int)std::max<int64_t>(1, s);
@@ -532,7 +840,13 @@ cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   if ((g.T + 127) / 128 > 65535 || (int64_t)g.groups * g.splits > 65535)
     return cudaErrorInvalidConfiguration;
-  if (g.tok_m) return g.bn == 256 ? launch_gemm<256, true>(g, stream) : launch_gemm<128, true>(g, stream);
+  if (g.tok_m && g.bn == 256) {
+    // (Tile rows of the scale maps are 32-bit coordinates.)
+    if (((int64_t)(g.T + 255) / 256 * 2 + 1) * (g.tok_k / 128) > 0x7FFFFFFF)
+      return cudaErrorInvalidConfiguration;
+    return g.part || g.splits != 1 ? cudaErrorInvalidValue : launch_pair(g, stream);
+  }
+  if (g.tok_m) return launch_gemm<128, true>(g, stream);
   switch (g.bn) {
     case 16: return launch_gemm<16, false>(g, stream);
     case 32: return launch_gemm<32, false>(g, stream);
