@@ -1238,11 +1238,11 @@ static csa_status check_proj_mx(const char* fn, int T, int H, int D, int g, int 
   return CSA_OK;
 }
 
-// Workspace: the operands of o and y (codes, scale tiles), the partials.
+// Workspace: the operands of o and y (codes, scale tiles).
 struct ProjPlanMx {
   csa::MxGemmPlan a, b;
-  size_t oq, os, yq, ys, part;
-  size_t total() const { return oq + os + yq + ys + part + 256; }
+  size_t oq, os, yq, ys;
+  size_t total() const { return oq + os + yq + ys + 256; }
 };
 
 static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g, int d_model) {
@@ -1255,9 +1255,6 @@ static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g, int d_model)
   pl.os = mxfp4_scale_bytes(T, hd);
   pl.yq = round_up((size_t)T * k2 / 2, 256);
   pl.ys = mxfp4_scale_bytes(T, k2);
-  const size_t p1 = pl.a.partials ? (size_t)pl.a.splits * T * k2 * 4 : 0;
-  const size_t p2 = pl.b.partials ? (size_t)pl.b.splits * T * d_model * 4 : 0;
-  pl.part = round_up(p1 > p2 ? p1 : p2, 256);
   return pl;
 }
 
@@ -1292,7 +1289,6 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   char* os = oq + pl.oq;
   char* yq = os + pl.os;
   char* ys = yq + pl.yq;
-  float* part = reinterpret_cast<float*>(ys + pl.ys);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t hd = (int64_t)H * D, k2 = (int64_t)g * d_g;
   // 1. o per token in 4 bits.
@@ -1312,7 +1308,6 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   a.tok_m = pl.a.tok_m;
   a.bn = pl.a.bn;
   a.splits = pl.a.splits;
-  a.part = pl.a.partials ? part : nullptr;
   a.c = y;
   a.yq = yq;
   a.ys = ys;
@@ -1334,7 +1329,6 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   b.tok_m = pl.b.tok_m;
   b.bn = pl.b.bn;
   b.splits = pl.b.splits;
-  b.part = pl.b.partials ? part : nullptr;
   b.c = z;
   b.status = dev_status;
   b.chained = 1;

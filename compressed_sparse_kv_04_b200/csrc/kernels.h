@@ -226,8 +226,7 @@ cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t 
 struct MxGemmPlan {
   int tok_m;       // tokens are the MMA's rows (else weights)
   int bn;          // the MMA's N
-  int splits;      // K splits
-  int partials;    // fp32 partials [splits, T, groups*N] are needed
+  int splits;      // K splits (the CTAs of a cluster)
 };
 MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms);
 struct MxGemm {
@@ -238,7 +237,6 @@ struct MxGemm {
   const void* w_scale;    // scale tiles
   int K, N, groups, T;
   int tok_m, bn, splits;  // see MxGemmPlan
-  float* part;            // partials, or null (tok_m and splits == 1)
   void* c;
   void *yq, *ys;
   int32_t* status;

@@ -24,13 +24,13 @@
 //
 // Two forms of one kernel (mx_gemm_kernel):
 //   - few tokens (T <= 128): weights are the MMA's M = 128 rows, tokens its N.
-//     The weights' bytes bound it: K is split so that two CTAs on every SM
-//     stream them; fp32 partials are summed by the kernel that quantises y
-//     (or stores z).
+//     The weights' bytes bound it.
 //   - more tokens: tokens are the M = 128 rows, weights N = 128, so that a
 //     thread of the epilogue holds one token's neighbouring features and
-//     quantises y in registers; K is split where the tiles do not fill the
-//     SMs (then y is quantised by the kernel that sums the partials).
+//     quantises y in registers.
+// Either way K is split over the CTAs of a cluster where the tiles alone do
+// not fill the SMs (two CTAs each); the CTAs add their sums up over shared
+// memory, in the order of the splits, and finish the tile's tokens
 // and a second kernel on CTA pairs for many tokens (mx_pair_kernel).
 #include <algorithm>
 #include <atomic>
@@ -94,7 +94,6 @@ struct GemmArgs {
   int64_t tok_tiles, w_tiles;  // scale tiles per 128 rows (of all groups; of one)
   int groups_k;              // token chunks between groups (= chunks)
   int N, splits, ldc;        // output features per group; K splits; features in all
-  float* part;               // [splits, T, ldc] fp32, or
   __nv_bfloat16* c;          // [T, ldc] bf16 or null, and with yq != null
   uint8_t* yq;               // codes [T, ldc/2] and
   uint8_t* ys;               // scale tiles [ceil(T/128), ldc/128, 512] of the bf16 values
@@ -135,6 +134,36 @@ CSA_DEV void store_scales(const GemmArgs& p, int t, int k, uint32_t word) {
                                (t % 32) * 16 + (t % 128) / 32 * 4) = word;
 }
 
+// Four values per lane, the 128 features of a tile row (k = its feature
+// 4 * lane): bf16 into c, and quantised into the next product's operand.
+CSA_DEV void store_quad(const GemmArgs& p, int t, int k, const float4& x, int lane) {
+  const uint32_t w[4] = {pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), 0u, 0u};
+  if (p.c) *reinterpret_cast<uint2*>(p.c + (int64_t)t * p.ldc + k) = make_uint2(w[0], w[1]);
+  if (!p.yq) return;
+  uint32_t am = mx_amax8(w);
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  am = max(am, __shfl_xor_sync(0xffffffffu, am, 4));
+  const uint32_t sb = mx_scale_byte(am);
+  *reinterpret_cast<uint16_t*>(p.yq + (int64_t)t * (p.ldc / 2) + k / 2) =
+      (uint16_t)mx_quantise8(w, sb);
+  uint32_t word = sb << (8 * (lane >> 3));
+  word |= __shfl_xor_sync(0xffffffffu, word, 8);
+  word |= __shfl_xor_sync(0xffffffffu, word, 16);
+  if (lane == 0) store_scales(p, t, k, word);
+}
+
+CSA_DEV float4 ld_cluster_v4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
+  return v;
+}
+
+constexpr int kSumRow = 132;  // floats per token of the sums (padded: spreads the banks)
+
 template <int BN, bool kTokM>
 struct Cfg {
   static constexpr int kABytes = BM * KB;
@@ -146,6 +175,7 @@ struct Cfg {
   static constexpr int kCols0 = (BN < 32 ? 32 : BN) + kStages * kScaleCols;
   static constexpr uint32_t kCols = kCols0 <= 128 ? 128 : 256;
   static_assert(BN <= 128 && kStages >= 2 && kCols0 <= 256, "tensor memory of two CTAs");
+  static_assert(kStages * (kABytes + kBBytes) >= (kTokM ? BM : BN) * kSumRow * 4, "the sums");
 };
 
 template <int BN, bool kTokM>
@@ -165,14 +195,15 @@ __global__ void __launch_bounds__(kThreads)
   uint64_t* done = drain + 1;           // one arrival per warp when its role is over
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sums = reinterpret_cast<float*>(smem);  // [tokens][kSumRow], over the ring
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int group = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
+  const int group = blockIdx.z, split = blockIdx.x % p.splits;
   // The chunks [k0, k1) of the group's inner dimension.
   const int k0 = (int)((int64_t)p.chunks * split / p.splits);
   const int nk = (int)((int64_t)p.chunks * (split + 1) / p.splits) - k0;
   const int w_tile = kTokM ? BN : BM, t_tile = kTokM ? BM : BN;
-  const int n0 = blockIdx.x * w_tile;   // first feature within the group
+  const int n0 = blockIdx.x / p.splits * w_tile;  // first feature within the group
   const int t0 = blockIdx.y * t_tile;   // first token
   const int w_row = group * p.N + n0;
 
@@ -285,35 +316,32 @@ __global__ void __launch_bounds__(kThreads)
     if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
       tc_fence_after();
       if constexpr (!kTokM) {
-        // Lane = feature, columns = tokens: one coalesced store per token.
-        const int col = w_row + 32 * q + lane;
-        float* dst = p.part + (int64_t)split * p.T * p.ldc + col;
+        // Lane = feature, columns = tokens.  (Every chunk has been consumed:
+        // the ring holds the sums.)
+        float* dst = sums + 32 * q + lane;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
+        for (int c = 0; c < BN && t0 + c < p.T; c += 16) {
           uint32_t v[16];
           tmem_ld16(acc + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (t0 + c + j < p.T) dst[(int64_t)(t0 + c + j) * p.ldc] = __uint_as_float(v[j]);
+          for (int j = 0; j < 16; ++j) dst[(c + j) * kSumRow] = __uint_as_float(v[j]);
         }
       } else {
         // Lane = token, columns = features.
         const int t = t0 + 32 * q + lane;
         const bool live = t < p.T;
-        if (p.part) {
-          float* dst = p.part + ((int64_t)split * p.T + t) * p.ldc + w_row;
+        if (p.splits > 1) {
+          float* dst = sums + (32 * q + lane) * kSumRow;
 #pragma unroll 1
           for (int c = 0; c < BN; c += 32) {
             uint32_t v[32];
             tmem_ld32(acc + c, v);
             tmem_wait_ld();
-            if (live) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4*>(dst + c + j) =
-                    make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            }
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(dst + c + j) =
+                  make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
         } else {
           uint32_t sw = 0;
@@ -343,6 +371,37 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
+  if (kTokM && p.splits == 1) return;
+  // The splits of a tile are one cluster: every CTA adds up some of the
+  // tile's tokens (in the order of the splits) over the cluster's shared
+  // memory and finishes them.  Every wait above is bounded, so every thread
+  // of every CTA arrives here.
+  __syncwarp();
+  const bool cluster = p.splits > 1;
+  if (cluster)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int nt = min(t_tile, p.T - t0);
+  for (int i = split + p.splits * warp; i < nt; i += p.splits * (kThreads / 32)) {
+    // Lane: features 4 * lane .. + 3 of token i.
+    const uint32_t at = smem_u32(sums + i * kSumRow + 4 * lane);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (cluster) {
+#pragma unroll 4
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 v = ld_cluster_v4(mapa(at, s));
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+      }
+    } else {
+      x = *reinterpret_cast<const float4*>(sums + i * kSumRow + 4 * lane);
+    }
+    store_quad(p, t0 + i, w_row + 4 * lane, x, lane);
+  }
+  if (cluster) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------- CTA pairs --
@@ -583,105 +642,58 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                  : "memory");
 }
 
-// Eight bf16 values of row t, columns 8*j .. +7 -> codes and, for every 16
-// lanes (128 columns), the word of their scale bytes.  All lanes take part.
-CSA_DEV void store_operand(uint8_t* codes, uint8_t* scales, int64_t cols, int64_t t, int64_t j,
-                           const uint32_t (&w)[4], bool live, int lane) {
-  uint32_t am = mx_amax8(w);
-  am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-  am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-  const uint32_t s = mx_scale_byte(am), cd = mx_quantise8(w, s);
-  uint32_t v = s << (8 * ((lane >> 2) & 3));
-  v |= __shfl_xor_sync(0xffffffffu, v, 4);
-  v |= __shfl_xor_sync(0xffffffffu, v, 8);
-  if (live) {
-    *reinterpret_cast<uint32_t*>(codes + t * (cols / 2) + 4 * j) = cd;
-    if ((lane & 15) == 0)
-      *reinterpret_cast<uint32_t*>(scales + ((t / 128) * (cols / 128) + j / 16) * kScaleTile +
-                                   (t % 32) * 16 + (t % 128) / 32 * 4) = v;
-  }
-}
-
-// Sum of the split partials [splits, T, cols] fp32, rounded to bf16: stored
-// (c) and, kQuant, quantised into the second product's operand.  Eight
-// columns per thread; cols is a multiple of 128.
-template <bool kQuant>
-__global__ void __launch_bounds__(256) mx_reduce_kernel(const float* __restrict__ part, int splits,
-                                                        int64_t n8, int64_t cols,
-                                                        __nv_bfloat16* __restrict__ c, uint8_t* yq,
-                                                        uint8_t* ys) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const bool live = i < n8;
-  pdl_trigger();
-  pdl_wait();  // the partials come from the GEMM kernel
-  float x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  if (live) {
-    const float* src = part + 8 * i;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(src + s * n8 * 8));
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(src + s * n8 * 8) + 1);
-      x[0] += a.x;
-      x[1] += a.y;
-      x[2] += a.z;
-      x[3] += a.w;
-      x[4] += b.x;
-      x[5] += b.y;
-      x[6] += b.z;
-      x[7] += b.w;
-    }
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-  if (live && c) reinterpret_cast<uint4*>(c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-  if constexpr (kQuant) {
-    const int64_t per = cols / 8;
-    store_operand(yq, ys, cols, i / per, i % per, w, live, threadIdx.x & 31);
-  }
-}
-
-// Rows of bf16 -> operand (codes and scale tiles).  blockIdx.x: 128 columns,
-// blockIdx.y: 128 rows; a warp reads two rows of 256 bytes at a time.  The
-// scale bytes of rows past the last one are written as zeros.
+// Rows of bf16 -> operand (codes and scale tiles).  blockIdx.x: 256 columns,
+// blockIdx.y: 128 rows, a warp per row: 512 bytes read and one full line of
+// codes written at a time.  The scale bytes of rows past the last one are
+// written as zeros.
 __global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* __restrict__ x,
                                                           int64_t ld_bytes, int64_t rows,
                                                           int64_t cols, uint8_t* codes,
                                                           uint8_t* scales) {
-  constexpr int kU = 8;  // rows of 16 threads each: 16 rows a step, 8 steps
-  __shared__ __align__(16) uint8_t sc[kScaleTile];
-  const int lane = threadIdx.x & 31, c = threadIdx.x & 15;
-  const int64_t r0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
-  const int rr = threadIdx.x >> 4;
-  const uint8_t* src = x + (r0 + rr) * ld_bytes + (k0 + 8 * c) * 2;
+  constexpr int kU = 8;  // rows in flight per warp
+  __shared__ __align__(16) uint8_t sc[2][kScaleTile];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 256;
+  const bool in = k0 + 8 * lane < cols;
+  const uint8_t* src = x + (r0 + warp) * ld_bytes + (k0 + 8 * lane) * 2;
+  uint8_t* dst = codes + (r0 + warp) * (cols / 2) + (k0 + 8 * lane) / 2;
   pdl_trigger();
-  uint4 v[kU];
+  const int live = (int)min((int64_t)128, rows - r0);
+  if (threadIdx.x < 2 * kScaleTile / 16)  // rows past the last one: zeros
+    reinterpret_cast<uint4*>(&sc[0][0])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+#pragma unroll 1
+  for (int g = 0; g < live; g += 8 * kU) {
+    uint4 v[kU];
 #pragma unroll
-  for (int u = 0; u < kU; ++u)
-    v[u] = r0 + rr + 16 * u < rows
-               ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)16 * u * ld_bytes))
-               : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < kU; ++u)
+      v[u] = in && warp + g + 8 * u < live
+                 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(g + 8 * u) * ld_bytes))
+                 : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    uint32_t am = mx_amax8(w);
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    const uint32_t s = mx_scale_byte(am), cd = mx_quantise8(w, s);
-    uint32_t b = s << (8 * ((lane >> 2) & 3));
-    b |= __shfl_xor_sync(0xffffffffu, b, 4);
-    b |= __shfl_xor_sync(0xffffffffu, b, 8);
-    const int r = rr + 16 * u;
-    if (r0 + r < rows)
-      *reinterpret_cast<uint32_t*>(codes + (r0 + r) * (cols / 2) + (k0 + 8 * c) / 2) = cd;
-    if (c == 0) *reinterpret_cast<uint32_t*>(sc + (r % 32) * 16 + r / 32 * 4) = b;
+    for (int u = 0; u < kU; ++u) {
+      const int r = warp + g + 8 * u;
+      if (r >= live) break;  // the same for the whole warp
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t am = mx_amax8(w);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const uint32_t s = mx_scale_byte(am), cd = mx_quantise8(w, s);
+      uint32_t b = s << (8 * ((lane >> 2) & 3));
+      b |= __shfl_xor_sync(0xffffffffu, b, 4);
+      b |= __shfl_xor_sync(0xffffffffu, b, 8);
+      if (in)
+        *reinterpret_cast<uint32_t*>(dst + (int64_t)(g + 8 * u) * (cols / 2)) = cd;
+      if ((lane & 15) == 0)
+        *reinterpret_cast<uint32_t*>(&sc[lane >> 4][(r % 32) * 16 + r / 32 * 4]) = b;
+    }
   }
   __syncthreads();
-  uint8_t* dst = scales + ((int64_t)blockIdx.y * (cols / 128) + blockIdx.x) * kScaleTile;
-  if (threadIdx.x < kScaleTile / 16)
-    reinterpret_cast<uint4*>(dst)[threadIdx.x] = reinterpret_cast<const uint4*>(sc)[threadIdx.x];
+  const int64_t tile = (int64_t)blockIdx.y * (cols / 128) + 2 * blockIdx.x;
+  const int i = threadIdx.x;  // 16 bytes of the two tiles each
+  if (i < 2 * kScaleTile / 16 && k0 + 128 * (i / (kScaleTile / 16)) < cols)
+    reinterpret_cast<uint4*>(scales + tile * kScaleTile)[i] =
+        reinterpret_cast<const uint4*>(&sc[0][0])[i];
 }
 
 template <int BN, bool kTokM>
@@ -706,7 +718,6 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
   p.N = g.N;
   p.splits = g.splits;
   p.ldc = g.groups * g.N;
-  p.part = g.part;
   p.c = static_cast<__nv_bfloat16*>(g.c);
   p.yq = static_cast<uint8_t*>(g.yq);
   p.ys = static_cast<uint8_t*>(g.ys);
@@ -718,17 +729,10 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
     for (int b = 16; b < BN; b <<= 1) ++slot;
   e = ensure_smem_attr(reinterpret_cast<const void*>(kern), slot, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(g.N / (kTokM ? BN : BM), (g.T + (kTokM ? BM : BN) - 1) / (kTokM ? BM : BN),
-                  g.groups * g.splits);
-  e = launch_pdl(kern, grid, dim3(kThreads), smem, stream, 0, g.chained, map_tok, map_w, p);
-  if (e != cudaSuccess || !g.part) return e;
-  const int64_t n8 = (int64_t)g.T * p.ldc / 8;
-  const dim3 rgrid((unsigned)((n8 + 255) / 256));
-  if (g.yq)
-    return launch_pdl(mx_reduce_kernel<true>, rgrid, dim3(256), 0, stream, 0, 1,
-                      (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
-  return launch_pdl(mx_reduce_kernel<false>, rgrid, dim3(256), 0, stream, 0, 1,
-                    (const float*)g.part, g.splits, n8, (int64_t)p.ldc, p.c, p.yq, p.ys);
+  const dim3 grid(g.N / (kTokM ? BN : BM) * g.splits,
+                  (g.T + (kTokM ? BM : BN) - 1) / (kTokM ? BM : BN), g.groups);
+  return launch_pdl(kern, grid, dim3(kThreads), smem, stream, g.splits > 1 ? g.splits : 0,
+                    g.chained, map_tok, map_w, p);
 }
 
 // Pairs of CTAs that can be resident at once on this device (one persistent
@@ -802,7 +806,7 @@ cudaError_t launch_pair(const MxGemm& g, cudaStream_t stream) {
 
 cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t cols, void* codes,
                                void* scales, cudaStream_t stream) {
-  const dim3 grid((unsigned)(cols / 128), (unsigned)((rows + 127) / 128));
+  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((rows + 127) / 128));
   return launch_pdl(mx_quantise_kernel, grid, dim3(256), 0, stream, 0, 0,
                     static_cast<const uint8_t*>(x), ld * 2, rows, cols,
                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
@@ -826,25 +830,27 @@ MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms) {
   }
   const int wt = pl.tok_m ? pl.bn : BM, tt = pl.tok_m ? BM : pl.bn;
   const int64_t tiles = (int64_t)(N / wt) * groups * ((T + tt - 1) / tt);
-  const int64_t slots = (int64_t)num_sms * 2;
-  // K splits: as many as fit beside each other, at least four chunks each.
-  int64_t s = std::min<int64_t>(slots / std::max<int64_t>(1, tiles), chunks / 4);
-  pl.splits = (int)std::max<int64_t>(1, s);
-  pl.partials = !pl.tok_m || pl.splits > 1;
+  // K splits: a power of two of CTAs (one cluster per tile), as many as fit
+  // beside each other (two on an SM; clusters leave some SMs of a GPC over),
+  // at least four chunks each.
+  pl.splits = 1;
+  while (pl.splits < 8 && 8 * tiles * pl.splits * 2 <= 7 * (int64_t)num_sms * 2 &&
+         chunks >= 4 * pl.splits * 2)
+    pl.splits *= 2;
   return pl;
 }
 
 cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t stream) {
   if (g.T < 1 || g.N % 128 || g.K % 256 || g.splits < 1 || g.splits > g.K / 256 ||
-      (!g.tok_m && (g.T > g.bn || !g.part)) || (g.bn == 256 && g.N % 256))
+      (!g.tok_m && g.T > g.bn) || (g.bn == 256 && g.N % 256))
     return cudaErrorInvalidValue;
-  if ((g.T + 127) / 128 > 65535 || (int64_t)g.groups * g.splits > 65535)
+  if ((g.T + 127) / 128 > 65535 || g.groups > 65535)
     return cudaErrorInvalidConfiguration;
   if (g.tok_m && g.bn == 256) {
     // (Tile rows of the scale maps are 32-bit coordinates.)
     if (((int64_t)(g.T + 255) / 256 * 2 + 1) * (g.tok_k / 128) > 0x7FFFFFFF)
       return cudaErrorInvalidConfiguration;
-    return g.part || g.splits != 1 ? cudaErrorInvalidValue : launch_pair(g, stream);
+    return g.splits != 1 ? cudaErrorInvalidValue : launch_pair(g, stream);
   }
   if (g.tok_m) return launch_gemm<128, true>(g, stream);
   switch (g.bn) {
