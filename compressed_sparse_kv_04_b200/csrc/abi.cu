@@ -1240,17 +1240,13 @@ static csa_status check_proj_mx(const char* fn, int T, int H, int D, int g, int 
 
 // Workspace: the operands of o and y (codes, scale tiles).
 struct ProjPlanMx {
-  csa::MxGemmPlan a, b;
   size_t oq, os, yq, ys;
   size_t total() const { return oq + os + yq + ys + 256; }
 };
 
-static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g, int d_model) {
+static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g) {
   ProjPlanMx pl{};
   const int64_t hd = (int64_t)H * D, k2 = (int64_t)g * d_g;
-  const int sms = csa::device_sm_count();
-  pl.a = csa::mx_gemm_plan(T, d_g, g, (int)(hd / g), sms);
-  pl.b = csa::mx_gemm_plan(T, d_model, 1, (int)k2, sms);
   pl.oq = round_up((size_t)T * hd / 2, 256);
   pl.os = mxfp4_scale_bytes(T, hd);
   pl.yq = round_up((size_t)T * k2 / 2, 256);
@@ -1261,7 +1257,7 @@ static ProjPlanMx proj_plan_mx(int T, int H, int D, int g, int d_g, int d_model)
 size_t grouped_out_proj_mxfp4_workspace_bytes(int T, int H, int D, int g, int d_g, int d_model) {
   if (check_proj_mx("grouped_out_proj_mxfp4_workspace_bytes", T, H, D, g, d_g, d_model) != CSA_OK)
     return 0;
-  return proj_plan_mx(T, H, D, g, d_g, d_model).total();
+  return proj_plan_mx(T, H, D, g, d_g).total();
 }
 
 csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_model, const void* o,
@@ -1279,7 +1275,7 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   OPT_PTR(y);
   REQ_PTR(z);
   OPT_PTR4(dev_status);
-  const ProjPlanMx pl = proj_plan_mx(T, H, D, g, d_g, d_model);
+  const ProjPlanMx pl = proj_plan_mx(T, H, D, g, d_g);
   const size_t need = pl.total();
   if (!ws || ws_bytes < need)
     return fail(CSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
@@ -1305,9 +1301,6 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   a.N = d_g;
   a.groups = g;
   a.T = T;
-  a.tok_m = pl.a.tok_m;
-  a.bn = pl.a.bn;
-  a.splits = pl.a.splits;
   a.c = y;
   a.yq = yq;
   a.ys = ys;
@@ -1326,9 +1319,6 @@ csa_status grouped_out_proj_mxfp4(int T, int H, int D, int g, int d_g, int d_mod
   b.N = d_model;
   b.groups = 1;
   b.T = T;
-  b.tok_m = pl.b.tok_m;
-  b.bn = pl.b.bn;
-  b.splits = pl.b.splits;
   b.c = z;
   b.status = dev_status;
   b.chained = 1;

@@ -223,12 +223,6 @@ cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t 
 // C[t, j*N + n] = sum_k tok[t, j*K + k] * W[j*N + n, k], fp32 accumulation,
 // rounded to bf16 (c, may be null with yq) and, with yq, quantised into the
 // operand (yq, ys) of the next product.
-struct MxGemmPlan {
-  int tok_m;       // tokens are the MMA's rows (else weights)
-  int bn;          // the MMA's N
-  int splits;      // K splits (the CTAs of a cluster)
-};
-MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms);
 struct MxGemm {
   const void* tok;        // codes [T, tok_k/2]
   const void* tok_scale;  // scale tiles
@@ -236,7 +230,6 @@ struct MxGemm {
   const void* w;          // codes [groups*N, K/2]
   const void* w_scale;    // scale tiles
   int K, N, groups, T;
-  int tok_m, bn, splits;  // see MxGemmPlan
   void* c;
   void *yq, *ys;
   int32_t* status;

@@ -716,7 +716,6 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
   p.w_tiles = g.K / 128;
   p.groups_k = p.chunks;
   p.N = g.N;
-  p.splits = g.splits;
   p.ldc = g.groups * g.N;
   p.c = static_cast<__nv_bfloat16*>(g.c);
   p.yq = static_cast<uint8_t*>(g.yq);
@@ -729,38 +728,46 @@ cudaError_t launch_gemm(const MxGemm& g, cudaStream_t stream) {
     for (int b = 16; b < BN; b <<= 1) ++slot;
   e = ensure_smem_attr(reinterpret_cast<const void*>(kern), slot, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(g.N / (kTokM ? BN : BM) * g.splits,
-                  (g.T + (kTokM ? BM : BN) - 1) / (kTokM ? BM : BN), g.groups);
-  return launch_pdl(kern, grid, dim3(kThreads), smem, stream, g.splits > 1 ? g.splits : 0,
-                    g.chained, map_tok, map_w, p);
+  const int x = g.N / (kTokM ? BN : BM), y = (g.T + (kTokM ? BM : BN) - 1) / (kTokM ? BM : BN);
+  // K splits (one cluster per tile): a power of two of CTAs, as many as fit
+  // beside each other (two on an SM; clusters leave some SMs of a GPC over),
+  // at least four chunks each.  8 tokens, 16 groups to 1024 and 7168 features
+  // (128 and 56 tiles, so 2 and 4 splits): 25.5 us; 28.9 with 1 and 2, 30.9
+  // with 4 and 2.
+  const int64_t slots = 2 * (int64_t)device_sm_count();
+  p.splits = 1;
+  while (p.splits < 8 && 8 * (int64_t)x * y * g.groups * p.splits * 2 <= 7 * slots &&
+         p.chunks >= 4 * p.splits * 2)
+    p.splits *= 2;
+  return launch_pdl(kern, dim3(x * p.splits, y, g.groups), dim3(kThreads), smem, stream,
+                    p.splits > 1 ? p.splits : 0, g.chained, map_tok, map_w, p);
 }
 
-// Pairs of CTAs that can be resident at once on this device (one persistent
-// pair each).
+// Pairs of CTAs that can be resident at once on the current device (one
+// persistent pair each); cached per device.
 int pairs_resident(size_t smem) {
   static std::atomic<int> cached[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return std::max(1, device_sm_count() / 2);
   int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();  // a refused query is not the caller's error
-      n = std::max(1, device_sm_count() / 2);
-    }
-    cached[dev].store(n, std::memory_order_relaxed);
+  if (n) return n;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();  // a refused query is not the caller's error
+    n = std::max(1, device_sm_count() / 2);
   }
+  cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -812,53 +819,19 @@ cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t 
                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
-MxGemmPlan mx_gemm_plan(int T, int N, int groups, int K, int num_sms) {
-  MxGemmPlan pl{};
-  const int chunks = K / 256;
-  if (T <= 128) {
-    pl.tok_m = 0;
-    pl.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-  } else {
-    // CTA pairs where their tiles (256 x 256) give every pair of SMs one.
-    const int64_t wide = (int64_t)(N / 256) * groups * ((T + 255) / 256);
-    pl.tok_m = 1;
-    pl.bn = N % 256 == 0 && wide >= num_sms / 2 ? 256 : 128;
-    if (pl.bn == 256) {
-      pl.splits = 1;
-      return pl;
-    }
-  }
-  const int wt = pl.tok_m ? pl.bn : BM, tt = pl.tok_m ? BM : pl.bn;
-  const int64_t tiles = (int64_t)(N / wt) * groups * ((T + tt - 1) / tt);
-  // K splits: a power of two of CTAs (one cluster per tile), as many as fit
-  // beside each other (two on an SM; clusters leave some SMs of a GPC over),
-  // at least four chunks each.
-  pl.splits = 1;
-  while (pl.splits < 8 && 8 * tiles * pl.splits * 2 <= 7 * (int64_t)num_sms * 2 &&
-         chunks >= 4 * pl.splits * 2)
-    pl.splits *= 2;
-  return pl;
-}
-
 cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t stream) {
-  if (g.T < 1 || g.N % 128 || g.K % 256 || g.splits < 1 || g.splits > g.K / 256 ||
-      (!g.tok_m && g.T > g.bn) || (g.bn == 256 && g.N % 256))
-    return cudaErrorInvalidValue;
-  if ((g.T + 127) / 128 > 65535 || g.groups > 65535)
-    return cudaErrorInvalidConfiguration;
-  if (g.tok_m && g.bn == 256) {
-    // (Tile rows of the scale maps are 32-bit coordinates.)
-    if (((int64_t)(g.T + 255) / 256 * 2 + 1) * (g.tok_k / 128) > 0x7FFFFFFF)
-      return cudaErrorInvalidConfiguration;
-    return g.splits != 1 ? cudaErrorInvalidValue : launch_pair(g, stream);
-  }
-  if (g.tok_m) return launch_gemm<128, true>(g, stream);
-  switch (g.bn) {
-    case 16: return launch_gemm<16, false>(g, stream);
-    case 32: return launch_gemm<32, false>(g, stream);
-    case 64: return launch_gemm<64, false>(g, stream);
-    default: return launch_gemm<128, false>(g, stream);
-  }
+  if (g.T < 1 || g.N % 128 || g.K % 256) return cudaErrorInvalidValue;
+  if ((g.T + 127) / 128 > 65535 || g.groups > 65535) return cudaErrorInvalidConfiguration;
+  if (g.T <= 16) return launch_gemm<16, false>(g, stream);
+  if (g.T <= 32) return launch_gemm<32, false>(g, stream);
+  if (g.T <= 64) return launch_gemm<64, false>(g, stream);
+  if (g.T <= 128) return launch_gemm<128, false>(g, stream);
+  // CTA pairs from the second tile of 256 tokens on (300 tokens, the sizes
+  // above: 57 us, 65 with single CTAs; 200 tokens: 49 us, 45).  (Tile rows of
+  // their scale maps are 32-bit coordinates.)
+  const bool fits = ((int64_t)(g.T + 255) / 256 * 2 + 1) * (g.tok_k / 128) <= 0x7FFFFFFF;
+  if (g.T > 256 && g.N % 256 == 0 && fits) return launch_pair(g, stream);
+  return launch_gemm<128, true>(g, stream);
 }
 
 }  // namespace csa
