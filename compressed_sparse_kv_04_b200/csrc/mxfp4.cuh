@@ -27,14 +27,8 @@ CSA_DEV uint32_t mx_scale_byte(uint32_t amax) {
   return e > 0 ? (uint32_t)e : 0u;
 }
 
-// 2^(127 - byte), the factor that brings a block's values into E2M1 range
-// (0 for a NaN block, whose codes are all zero).
-CSA_DEV float mx_inv_scale(uint32_t byte) {
-  return byte >= 254u ? 0.f : __uint_as_float((254u - byte) << 23);
-}
-
-// Eight fp32 values (already scaled) -> eight codes, value i in bits 4i.
-CSA_DEV uint32_t mx_codes8(const float (&x)[8]) {
+// Eight fp32 values (pairs) -> eight codes, value i in bits 4i.
+CSA_DEV uint32_t mx_codes8(const float2 (&x)[4]) {
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -43,20 +37,21 @@ CSA_DEV uint32_t mx_codes8(const float (&x)[8]) {
       "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(w)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x),
+        "f"(x[3].y));
   return w;
 }
 
 // Eight bf16 values (pairs) of a block with scale byte `s` -> codes.
 CSA_DEV uint32_t mx_quantise8(const uint32_t (&w)[4], uint32_t s) {
-  const float f = mx_inv_scale(s);
-  float x[8];
+  // 2^(127 - s) brings the block into E2M1 range (s <= 253 for finite blocks).
+  const float f = __uint_as_float((254u - min(s, 253u)) << 23);
+  const float2 f2 = make_float2(f, f);
+  float2 x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = s == 255u ? 0.f : bf16_lo(w[i]) * f;
-    x[2 * i + 1] = s == 255u ? 0.f : bf16_hi(w[i]) * f;
-  }
-  return mx_codes8(x);
+  for (int i = 0; i < 4; ++i) x[i] = mul_f32x2(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), f2);
+  const uint32_t c = mx_codes8(x);
+  return s == 255u ? 0u : c;  // a NaN block's codes are zero
 }
 
 // Largest magnitude of eight bf16 values, as bf16 bits (integer order of the
@@ -78,14 +73,10 @@ CSA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // exponent becomes a bf16 subnormal, which the multiply keeps), so the value
 // is that times 2^126 * 2^(s-127) = 2^(s-1): one exact product for
 // s <= 128, and a second factor 2^(s-128) (NaN for s = 255) above.
-struct MxScale {
-  uint32_t lo, hi;
-  CSA_DEV explicit MxScale(uint32_t s) {
-    const uint32_t l = min(s, 128u);
-    lo = ((l + 126u) << 7) * 0x10001u;
-    hi = (s == 255u ? 0x7FC0u : (s - l + 127u) << 7) * 0x10001u;
-  }
-};
+CSA_DEV uint32_t mx_bf16_lo(uint32_t s) { return ((min(s, 128u) + 126u) << 7) * 0x10001u; }
+CSA_DEV uint32_t mx_bf16_hi(uint32_t s) {
+  return (s == 255u ? 0x7FC0u : (max(s, 128u) - 1u) << 7) * 0x10001u;
+}
 
 // Eight codes (value i in bits 4i) -> eight bf16 values times `lo` as four
 // pairs.  The high nibble of a byte of w << 4 (w) is the even (odd) code of
