@@ -93,6 +93,13 @@ struct MCfg {
   static constexpr uint32_t kAlloc = (D <= 256 && kQCol + D / 2 <= 256) ? 256 : 512;
 };
 
+// Whether a kernel can merge a row's splits inside a cluster.  Over an MXFP4
+// cache at D = 512 the merge kernel, which overlaps its start with the
+// attention's end, is faster (5 rows of 64 heads: 17.7 us against 20.3; 8 rows
+// 18.3, 20.5); at D = 128 the cluster is (10.2 us against 10.8).
+template <int D, bool kMx>
+constexpr bool kClusterMerge = !kMx || D == 128;
+
 struct Meta {
   int32_t grow[TN];   // row coordinate in the tensor map
   int32_t pos[TN];    // RoPE position
@@ -187,6 +194,33 @@ CSA_DEV bool wait_all(uint64_t* bar, uint32_t parity, const Params& p, volatile 
   return __all_sync(0xffffffffu, ok);
 }
 
+// Where a merge finds the split partials of one (row, head): lane l's dims
+// (fp16) and the (max, sum) pair of each split.
+// kLdg: they come from an earlier kernel (read-only path); otherwise they were
+// written during this kernel by other CTAs and are read from L2.
+template <int D, bool kLdg>
+struct Partials {
+  const __half* src;  // split 0's dims of this lane
+  const float* ml;    // split 0's maximum of this head
+  int64_t stride;     // halves between splits
+  int H;
+  CSA_DEV Partials(const Params& p, int row, int h, int lane)
+      : src(p.part_o + ((int64_t)row * p.splits * p.H + h) * D + lane * (D / 32)),
+        ml(p.part_ml + (int64_t)row * p.splits * 2 * p.H + h), stride((int64_t)p.H * D), H(p.H) {}
+  template <typename T>
+  CSA_DEV static T ld(const T* a) {
+    return kLdg ? __ldg(a) : __ldcg(a);
+  }
+  CSA_DEV float maximum(int s) const { return ld(ml + (int64_t)s * 2 * H); }
+  CSA_DEV float sum(int s) const { return ld(ml + (int64_t)s * 2 * H + H); }
+  CSA_DEV uint4 load16(int s, int i) const {
+    return ld(reinterpret_cast<const uint4*>(src + (int64_t)s * stride) + i);
+  }
+  CSA_DEV uint2 load8(int s) const {
+    return ld(reinterpret_cast<const uint2*>(src + (int64_t)s * stride));
+  }
+};
+
 // Merge of the split partials of one (row, head) by one warp: fold in the
 // sink, normalise, apply the inverse rotation, store bf16 (and the
 // log-sum-exp).  Lane l owns dims [l*VPL, (l+1)*VPL) (VPL = D/32), so the
@@ -196,27 +230,19 @@ CSA_DEV bool wait_all(uint64_t* bar, uint32_t parity, const Params& p, volatile 
 // memory).  The first G splits' partials are loaded together with the
 // (max, sum) pairs, so that with S <= G the warp waits on one round of L2
 // reads; further groups of G follow one round each.
-// kLdg: the partials come from an earlier kernel (read-only path); otherwise
-// they were written during this kernel by other CTAs and are read from L2.
 template <int D, int R, int G, bool kLdg>
 CSA_DEV void merge_head(const Params& p, int row, int h, int lane, float* wsplit) {
+  const Partials<D, kLdg> src(p, row, h, lane);
   constexpr int VPL = D / 32;     // dims per lane: 16 (D = 512) or 4 (D = 128)
   constexpr int NW = VPL / 2;     // 32-bit words (fp16 pairs) per lane and split
   static_assert(VPL == 16 || VPL == 4, "D must be 512 or 128");
   const int S = p.splits;
-  const float* ml = p.part_ml + (int64_t)row * S * 2 * p.H;
-  const __half* src = p.part_o + ((int64_t)row * S * p.H + h) * D + lane * VPL;
-  const int64_t stride = (int64_t)p.H * D;
-  auto ld4 = [](const uint4* a) -> uint4 { return kLdg ? __ldg(a) : __ldcg(a); };
-  auto ld2 = [](const uint2* a) -> uint2 { return kLdg ? __ldg(a) : __ldcg(a); };
-  auto ldf = [](const float* a) -> float { return kLdg ? __ldg(a) : __ldcg(a); };
   auto load = [&](int s, uint32_t (&v)[NW]) {
-    const __half* a = src + (int64_t)s * stride;
     if constexpr (VPL == 16) {
-      *reinterpret_cast<uint4*>(&v[0]) = ld4(reinterpret_cast<const uint4*>(a));
-      *reinterpret_cast<uint4*>(&v[4]) = ld4(reinterpret_cast<const uint4*>(a) + 1);
+      *reinterpret_cast<uint4*>(&v[0]) = src.load16(s, 0);
+      *reinterpret_cast<uint4*>(&v[4]) = src.load16(s, 1);
     } else {
-      *reinterpret_cast<uint2*>(&v[0]) = ld2(reinterpret_cast<const uint2*>(a));
+      *reinterpret_cast<uint2*>(&v[0]) = src.load8(s);
     }
   };
   uint32_t buf[G][NW];
@@ -226,21 +252,21 @@ CSA_DEV void merge_head(const Params& p, int row, int h, int lane, float* wsplit
   // Split `lane`'s (max, sum) pair, in flight with the partials.
   float m0 = -INFINITY, l0 = 0.f;
   if (lane < S) {
-    m0 = ldf(ml + (int64_t)lane * 2 * p.H + h);
-    l0 = ldf(ml + (int64_t)lane * 2 * p.H + p.H + h);
+    m0 = src.maximum(lane);
+    l0 = src.sum(lane);
   }
   const float LOG2E = 1.4426950408889634f;
   const float z = p.sink[h];
   const float z2 = z * LOG2E;  // log2 domain
   float M = fmaxf(z2, m0);
-  for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, ldf(ml + (int64_t)s * 2 * p.H + h));
+  for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, src.maximum(s));
   M = warp_max(M);
   const bool zero = z == INFINITY || M == -INFINITY;  // +inf sink, or nothing to attend
   float L = 0.f;
   if (!zero) {
     for (int s = lane; s < S; s += 32) {
-      const float ms = s == lane ? m0 : ldf(ml + (int64_t)s * 2 * p.H + h);
-      const float ls = s == lane ? l0 : ldf(ml + (int64_t)s * 2 * p.H + p.H + h);
+      const float ms = s == lane ? m0 : src.maximum(s);
+      const float ls = s == lane ? l0 : src.sum(s);
       const float w = ms == -INFINITY ? 0.f : ls * exp2f(ms - M);
       wsplit[s] = w;  // the split's stored output is O / l
       L += w;
@@ -1269,7 +1295,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         }
       }
       if (head_ok) {
-        if (p.cluster_merge && !p.fused) {
+        if (kClusterMerge<D, kMx> && p.cluster_merge && !p.fused) {
           // Plain stores: the other CTAs of the cluster read the partial
           // back after the cluster barrier below.
           const uint4* s4 = reinterpret_cast<const uint4*>(ob);
@@ -1305,7 +1331,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kAlloc);
   }
-  if (p.cluster_merge) {
+  if (kClusterMerge<D, kMx> && p.cluster_merge) {
     // Every CTA of the cluster (the S splits of this head group) has written
     // its partial and its (max, sum): the release / acquire cluster barrier
     // publishes them, and CTA `split` then merges heads split, split + S, ...
@@ -1423,7 +1449,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   // The splits of each head group form one cluster and merge in-kernel, when
   // every cluster of the launch can be resident at once (otherwise the
   // clusters would run in waves: the separate merge kernel is faster).
-  if (!p.fused && !a.emit_partials &&
+  if (kClusterMerge<D, kMx> && !p.fused && !a.emit_partials &&
       (int64_t)cps * rows <=
           clusters_resident(reinterpret_cast<const void*>(kern), variant, kBlockThreads<kMx>,
                             a.splits, smem)) {
