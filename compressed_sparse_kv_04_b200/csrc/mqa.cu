@@ -230,8 +230,18 @@ struct Partials {
 // memory).  The first G splits' partials are loaded together with the
 // (max, sum) pairs, so that with S <= G the warp waits on one round of L2
 // reads; further groups of G follow one round each.
+// The rotation angle of pair `lane` at the row's position.
+template <int R>
+CSA_DEV float2 row_angle(const Params& p, int row, int lane) {
+  float sn = 0.f, cs = 1.f;
+  if (R > 0 && lane < R / 2)
+    sincos_reduced((double)row_pos(p, row) * p.inv_freq[lane], &sn, &cs);
+  return make_float2(sn, cs);
+}
+
 template <int D, int R, int G, bool kLdg>
-CSA_DEV void merge_head(const Params& p, int row, int h, int lane, float* wsplit) {
+CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, int lane,
+                        float* wsplit) {
   const Partials<D, kLdg> src(p, row, h, lane);
   constexpr int VPL = D / 32;     // dims per lane: 16 (D = 512) or 4 (D = 128)
   constexpr int NW = VPL / 2;     // 32-bit words (fp16 pairs) per lane and split
@@ -256,7 +266,6 @@ CSA_DEV void merge_head(const Params& p, int row, int h, int lane, float* wsplit
     l0 = src.sum(lane);
   }
   const float LOG2E = 1.4426950408889634f;
-  const float z = p.sink[h];
   const float z2 = z * LOG2E;  // log2 domain
   float M = fmaxf(z2, m0);
   for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, src.maximum(s));
@@ -307,9 +316,9 @@ CSA_DEV void merge_head(const Params& p, int row, int h, int lane, float* wsplit
       constexpr int K = R / 2 / VPL;  // lanes per rotated half
       constexpr int L0 = 32 - 2 * K;  // first lane holding rotated dims
       static_assert(K >= 1 && (K & (K - 1)) == 0, "rotated halves must span whole lanes");
-      const int64_t pos = row_pos(p, row);
-      float sn = 0.f, cs = 1.f;
-      if (lane < R / 2) sincos_reduced((double)pos * p.inv_freq[lane], &sn, &cs);
+      // (kLdg: the merge kernel formed the angles before its wait.)
+      if (!kLdg) angle = row_angle<R>(p, row, lane);
+      const float sn = angle.x, cs = angle.y;
       const bool rot = lane >= L0;
       const bool first = rot && lane - L0 < K;
       const int jb = rot ? ((lane - L0) % K) * VPL : 0;
@@ -342,11 +351,16 @@ template <int D, int R, int G>
 __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int rows) {
   extern __shared__ float wsm[];  // [4 warps][S] split weights
   pdl_trigger();
-  pdl_wait();  // the partials come from the attention kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t gw = (int64_t)blockIdx.x * 4 + warp;
-  if (gw >= (int64_t)rows * p.H) return;
-  merge_head<D, R, G, true>(p, (int)(gw / p.H), (int)(gw % p.H), lane, wsm + warp * p.splits);
+  const bool live = gw < (int64_t)rows * p.H;
+  const int row = live ? (int)(gw / p.H) : 0, h = live ? (int)(gw % p.H) : 0;
+  // Caller inputs, read and turned into angles while the attention still runs.
+  const float z = p.sink[h];
+  const float2 angle = row_angle<R>(p, row, lane);
+  pdl_wait();  // the partials come from the attention kernel
+  if (!live) return;
+  merge_head<D, R, G, true>(p, z, angle, row, h, lane, wsm + warp * p.splits);
 }
 
 template <int D, int R, bool kMx>
@@ -1343,7 +1357,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     const int nh = pair ? min(HC, p.H - hg0) : p.H;
     float* wsplit = reinterpret_cast<float*>(stages) + warp * 32;  // S <= 16 weights
     for (int j = split + p.splits * warp; j < nh; j += p.splits * NW)
-      merge_head<D, R, 4, false>(p, row, hg0 + j, lane, wsplit);
+      merge_head<D, R, 4, false>(p, p.sink[hg0 + j], make_float2(0.f, 1.f), row, hg0 + j, lane,
+                                 wsplit);
   }
 }
 
