@@ -35,11 +35,11 @@
 //     rescaled in TMEM only when the running max grows by more than 8) and
 //     write P (bf16) to shared memory in the MMA's K-major layout.
 // Splits of the KV list run on different CTAs; their (m, l, O) partials are
-// merged, with the sink folded in and the inverse RoPE applied, by the CTAs
-// themselves when the S splits of a head group form one thread-block
-// cluster and all clusters of the launch fit at once (S <= 16: a cluster
-// barrier, then each CTA merges a share of the heads from L2), else by
-// mqa_combine_kernel.  With one split per row the
+// merged, with the sink folded in and the inverse RoPE applied, by
+// mqa_combine_kernel, or at D = 128 by the CTAs themselves when the S splits
+// of a head group form one thread-block cluster and all clusters of the
+// launch fit at once (S <= 16: a cluster barrier, then each CTA merges a share
+// of the heads from L2).  With one split per row the
 // attention CTA finishes its rows directly.  Every wait is bounded and
 // reports CSA_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
@@ -93,12 +93,13 @@ struct MCfg {
   static constexpr uint32_t kAlloc = (D <= 256 && kQCol + D / 2 <= 256) ? 256 : 512;
 };
 
-// Whether a kernel can merge a row's splits inside a cluster.  Over an MXFP4
-// cache at D = 512 the merge kernel, which overlaps its start with the
-// attention's end, is faster (5 rows of 64 heads: 17.7 us against 20.3; 8 rows
-// 18.3, 20.5); at D = 128 the cluster is (10.2 us against 10.8).
-template <int D, bool kMx>
-constexpr bool kClusterMerge = !kMx || D == 128;
+// Whether a kernel can merge a row's splits inside a cluster.  At D = 512 the
+// merge kernel, which overlaps its start with the attention's end, is faster
+// (4-bit cache, 5 rows of 64 heads: 17.7 us against 20.3; the V4-Flash decode
+// step 42.5 us against 46.4, the 1M one 71.8 against 73.0); at D = 128 the
+// cluster is (10.2 us against 10.8).
+template <int D>
+constexpr bool kClusterMerge = D == 128;
 
 struct Meta {
   int32_t grow[TN];   // row coordinate in the tensor map
@@ -266,6 +267,7 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
     l0 = src.sum(lane);
   }
   const float LOG2E = 1.4426950408889634f;
+  if (!kLdg) z = p.sink[h];  // (the merge kernel read it before its wait)
   const float z2 = z * LOG2E;  // log2 domain
   float M = fmaxf(z2, m0);
   for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, src.maximum(s));
@@ -316,7 +318,6 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
       constexpr int K = R / 2 / VPL;  // lanes per rotated half
       constexpr int L0 = 32 - 2 * K;  // first lane holding rotated dims
       static_assert(K >= 1 && (K & (K - 1)) == 0, "rotated halves must span whole lanes");
-      // (kLdg: the merge kernel formed the angles before its wait.)
       if (!kLdg) angle = row_angle<R>(p, row, lane);
       const float sn = angle.x, cs = angle.y;
       const bool rot = lane >= L0;
@@ -1335,7 +1336,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         }
       }
       if (head_ok) {
-        if (kClusterMerge<D, kMx> && p.cluster_merge && !p.fused) {
+        if (kClusterMerge<D> && p.cluster_merge && !p.fused) {
           // Plain stores: the other CTAs of the cluster read the partial
           // back after the cluster barrier below.
           const uint4* s4 = reinterpret_cast<const uint4*>(ob);
@@ -1371,7 +1372,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kAlloc);
   }
-  if (kClusterMerge<D, kMx> && p.cluster_merge) {
+  if (kClusterMerge<D> && p.cluster_merge) {
     // Every CTA of the cluster (the S splits of this head group) has written
     // its partial and its (max, sum): the release / acquire cluster barrier
     // publishes them, and CTA `split` then merges heads split, split + S, ...
@@ -1383,8 +1384,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     const int nh = pair ? min(HC, p.H - hg0) : p.H;
     float* wsplit = reinterpret_cast<float*>(stages) + warp * 32;  // S <= 16 weights
     for (int j = split + p.splits * warp; j < nh; j += p.splits * NW)
-      merge_head<D, R, 4, false>(p, p.sink[hg0 + j], make_float2(0.f, 1.f), row, hg0 + j, lane,
-                                 wsplit);
+      merge_head<D, R, 4, false>(p, 0.f, make_float2(0.f, 1.f), row, hg0 + j, lane, wsplit);
   }
 }
 
@@ -1490,7 +1490,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   // The splits of each head group form one cluster and merge in-kernel, when
   // every cluster of the launch can be resident at once (otherwise the
   // clusters would run in waves: the separate merge kernel is faster).
-  if (kClusterMerge<D, kMx> && !p.fused && !a.emit_partials &&
+  if (kClusterMerge<D> && !p.fused && !a.emit_partials &&
       (int64_t)cps * rows <=
           clusters_resident(reinterpret_cast<const void*>(kern), variant, kBlockThreads<kMx>,
                             a.splits, smem)) {
