@@ -128,10 +128,13 @@ CSA_DEV uint32_t store_block(const GemmArgs& p, int t, int k, const uint32_t* v,
         make_uint4(cd[0], cd[1], cd[2], cd[3]);
   return sb;
 }
-// The four scale bytes of columns k .. k + 127 (k a multiple of 128).
+// Where the four scale bytes of token t, columns k/128*128 .. + 127 are.
+CSA_DEV uint8_t* scale_word_at(const GemmArgs& p, int t, int k) {
+  return p.ys + ((int64_t)(t / 128) * (p.ldc / 128) + k / 128) * kScaleTile + (t % 32) * 16 +
+         (t % 128) / 32 * 4;
+}
 CSA_DEV void store_scales(const GemmArgs& p, int t, int k, uint32_t word) {
-  *reinterpret_cast<uint32_t*>(p.ys + ((int64_t)(t / 128) * (p.ldc / 128) + k / 128) * kScaleTile +
-                               (t % 32) * 16 + (t % 128) / 32 * 4) = word;
+  *reinterpret_cast<uint32_t*>(scale_word_at(p, t, k)) = word;
 }
 
 // Four values per lane, the 128 features of a tile row (k = its feature
@@ -411,7 +414,9 @@ __global__ void __launch_bounds__(kThreads)
 // where each CTA loads a whole 256-row weight tile: that form was bound by L2
 // at 12 TB/s).  The grid is persistent (one CTA per SM); the epilogue's eight
 // warps take the accumulator into registers at once, so the next tile's MMAs
-// start while they convert and store it.
+// start while they convert and store it.  Where the last round of tiles would
+// leave half of the pairs or more idle, its tiles are cut into two of 128
+// features.
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 struct Pair {
   static constexpr int kStages = 6;
@@ -422,6 +427,17 @@ struct Pair {
   static constexpr int kAccCols = 256;
   static constexpr uint32_t kCols = 512;
   static_assert(kAccCols + kStages * kScaleCols <= 512, "tensor memory");
+};
+
+// Work item i of the launch: a whole tile, or (the last round) half of one.
+struct PairItem {
+  int m, n, half;  // half: 0 / 1, or -1 for a whole tile
+  CSA_DEV PairItem(int i, int m_tiles, int whole) {
+    half = i < whole ? -1 : (i - whole) & 1;
+    const int tile = i < whole ? i : whole + ((i - whole) >> 1);
+    m = tile % m_tiles;
+    n = tile / m_tiles;
+  }
 };
 
 CSA_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
@@ -480,6 +496,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int m_tiles = (p.T + 255) / 256, n_group = p.N / 256;
   const int tiles = m_tiles * (p.ldc / 256);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // Items [0, whole) are tiles, the others halves of the remaining ones.
+  const int rest = tiles % step;
+  const int whole = 2 * rest <= step ? tiles - rest : tiles;
+  const int items = whole + 2 * (tiles - whole);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -517,9 +537,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       pdl_wait();
       int it = 0;
       bool ok = true;
-      for (int tile = first; ok && tile < tiles; tile += step) {
-        const int m = tile % m_tiles, n = tile / m_tiles;
-        const int kg = n / n_group * p.chunks;  // the group's first token chunk
+      for (int i = first; ok && i < items; i += step) {
+        const PairItem w(i, m_tiles, whole);
+        const int kg = w.n / n_group * p.chunks;  // the group's first token chunk
+        // Half a tile: 64 weight rows each (the box loads 64 more, unused).
+        const int w_row = w.n * 256 + (w.half < 0 ? rank * 128 : w.half * 128 + rank * 64);
+        const int ts_row = (int32_t)((2 * w.m + rank) * p.tok_tiles) + 2 * kg;
+        const int ws_row0 = (int32_t)((2 * w.n + max(w.half, 0)) * p.w_tiles);
+        const int ws_row1 = (int32_t)((2 * w.n + 1) * p.w_tiles);
         for (int c = 0; c < p.chunks; ++c, ++it) {
           const int s = it % C::kStages;
           if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, p.status, abort_flag)) {
@@ -529,15 +554,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           uint8_t* st = smem + s * 2 * C::kOperand;
           uint8_t* sc = scales + s * C::kScaleBytes;
           if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStageBytes);
-          tma_load_2d_pair(st, &map_tok, &full[s], (kg + c) * KB, m * 256 + rank * 128);
-          tma_load_2d_pair(st + C::kOperand, &map_w, &full[s], c * KB, n * 256 + rank * 128);
+          tma_load_2d_pair(st, &map_tok, &full[s], (kg + c) * KB, w.m * 256 + rank * 128);
+          tma_load_2d_pair(st + C::kOperand, &map_w, &full[s], c * KB, w_row);
           // (Scale tiles past the last token lie past the map: zeros.)
-          tma_load_2d_pair(sc, &map_ts, &full[s], 0,
-                           (int32_t)((2 * m + rank) * p.tok_tiles) + 2 * (kg + c));
-          tma_load_2d_pair(sc + 2 * kScaleTile, &map_ws, &full[s], 0,
-                           (int32_t)(2 * n * p.w_tiles) + 2 * c);
-          tma_load_2d_pair(sc + 4 * kScaleTile, &map_ws, &full[s], 0,
-                           (int32_t)((2 * n + 1) * p.w_tiles) + 2 * c);
+          tma_load_2d_pair(sc, &map_ts, &full[s], 0, ts_row + 2 * c);
+          tma_load_2d_pair(sc + 2 * kScaleTile, &map_ws, &full[s], 0, ws_row0 + 2 * c);
+          tma_load_2d_pair(sc + 4 * kScaleTile, &map_ws, &full[s], 0, ws_row1 + 2 * c);
         }
       }
       if (*abort_flag) {  // copies still in flight land before the CTA exits
@@ -558,7 +580,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t t_scale = tmem + C::kAccCols;
       bool issued = false, ok = true;
       int it = 0, j = 0;
-      for (int tile = first; ok && tile < tiles; tile += step, ++j) {
+      for (int i = first; ok && i < items; i += step, ++j) {
+        const bool half = i >= whole;
         if (j > 0) {
           ok = mbar_wait<true>(acce, (j - 1) & 1, p.status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
@@ -578,14 +601,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int h = 0; h < 2; ++h) {
               copy_scales_pair(ta + 4 * h, desc_scale(sc + h * kScaleTile));
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                copy_scales_pair(tb + 8 * h + 4 * i,
-                                 desc_scale(sc + ((1 + i) * 2 + h) * kScaleTile));
+              for (int b = 0; b < 2; ++b)
+                copy_scales_pair(tb + 8 * h + 4 * b,
+                                 desc_scale(sc + ((1 + b) * 2 + h) * kScaleTile));
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_mxf4_pair(tmem, desc_kmaj(ab + kk * 32), desc_kmaj(bb + kk * 32),
-                            idesc_mxf4(256, 256, 2 * (kk & 1)), ta + 4 * (kk >> 1),
+                            idesc_mxf4(256, half ? 128 : 256, 2 * (kk & 1)), ta + 4 * (kk >> 1),
                             tb + 8 * (kk >> 1), (c > 0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(&empty[s]);
             if (c == p.chunks - 1) mma_commit_pair(accf);
@@ -606,29 +629,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- epilogue --
-    // Two warps per lane quarter, 128 columns each; lane = token.
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
+    // Two warps per lane quarter, 128 columns each (64 of a half tile); lane =
+    // token.
+    const int q = warp & 3, side = (warp - 2) >> 2;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t acce0 = mapa(smem_u32(acce), 0);
     int j = 0;
-    for (int tile = first; tile < tiles; tile += step, ++j) {
+    for (int i = first; i < items; i += step, ++j) {
+      const PairItem w(i, m_tiles, whole);
       const bool ok = mbar_wait<true>(accf, j & 1, p.status, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      const int cols = w.half < 0 ? 128 : 64;
       uint32_t v[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(acc + 32 * c, v[c]);
+      for (int c = 0; c < 4; ++c)
+        if (32 * c < cols) tmem_ld32(acc + side * cols + 32 * c, v[c]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(acce0);
-      const int t = tile % m_tiles * 256 + rank * 128 + 32 * q + lane;
-      const int k = tile / m_tiles * 256 + 128 * half;
+      const int t = w.m * 256 + rank * 128 + 32 * q + lane;
+      const int k = w.n * 256 + max(w.half, 0) * 128 + side * cols;
       const bool live = t < p.T;
       uint32_t sw = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) sw |= store_block(p, t, k + 32 * c, v[c], live) << (8 * c);
-      if (live && p.yq) store_scales(p, t, k, sw);
+      for (int c = 0; c < 4; ++c)
+        if (32 * c < cols) sw |= store_block(p, t, k + 32 * c, v[c], live) << (8 * c);
+      if (live && p.yq) {
+        if (w.half < 0)
+          store_scales(p, t, k, sw);
+        else
+          *reinterpret_cast<uint16_t*>(scale_word_at(p, t, k) + 2 * side) = (uint16_t)sw;
+      }
     }
   }
   // Every wait above is bounded, so every thread of both CTAs arrives here;
@@ -804,7 +837,8 @@ cudaError_t launch_pair(const MxGemm& g, cudaStream_t stream) {
   e = ensure_smem_attr(reinterpret_cast<const void*>(mx_pair_kernel), 31, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((g.T + 255) / 256) * (p.ldc / 256);
-  const int pairs = (int)std::min<int64_t>(tiles, pairs_resident(smem));
+  // Up to twice as many pairs as tiles: those of a last round may be halved.
+  const int pairs = (int)std::min<int64_t>(2 * tiles, pairs_resident(smem));
   return launch_pdl(mx_pair_kernel, dim3(2 * pairs), dim3(kPairThreads), smem, stream, 2, g.chained,
                     map_tok, map_w, map_ts, map_ws, p);
 }
