@@ -477,6 +477,10 @@ def mxfp4_cache(p, N_cap, device=None):
 
 
 _ROW_BYTES = {}
+_Tensor = torch.Tensor
+# (None in a torch built without CUDA: only CUDA tensors reach them.)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _row_bytes(d):
@@ -492,8 +496,8 @@ def _need(t, name, dtype, *shape):
     if t is None:
         return None
     # The usual case in few steps: a decode step makes a dozen of these checks.
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and
-            t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice()):
+    if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+            t.is_cuda and t.get_device() == _current_device()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
@@ -514,7 +518,7 @@ def _size(t, name, dim):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
     if t.dim() <= dim:
         raise ValueError(f"{name} has {t.dim()} dimensions")
-    return t.shape[dim]
+    return t.size(dim)
 
 
 def _need_cache(p, kv4):
@@ -526,13 +530,13 @@ def _need_tok(p, kv_tok):
 
 
 def _status(dev_status):
-    return _need(dev_status, "dev_status", torch.int32, 1)
+    return None if dev_status is None else _need(dev_status, "dev_status", torch.int32, 1)
 
 
 def _raw_stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _current_stream(_current_device())
 
 
 def _is_mxfp4(p, kv_c, kv_tok):
@@ -550,21 +554,19 @@ def _ws(ws):
 def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
     """Quantises rows [B, n, d] (bf16; each sequence's rows contiguous) into
     entries first_entry[b] + i, i < count[b], of kv4."""
-    n = _size(rows, "rows", 1)
-    if rows.dtype != torch.bfloat16 or rows.shape != (p.B, n, p.d):
-        raise ValueError(f"rows must be bfloat16 [{p.B}, n, {p.d}], not {rows.dtype} "
+    B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
+    if rows.dtype is not torch.bfloat16 or rows.shape != (B, n, d):
+        raise ValueError(f"rows must be bfloat16 [{B}, n, {d}], not {rows.dtype} "
                          f"{list(rows.shape)}")
     seq, row, one = rows.stride()
-    if n and (one != 1 or (n > 1 and row != p.d)):
+    if n and (one != 1 or (n > 1 and row != d)):
         raise ValueError("each sequence's rows must be contiguous")
-    if not rows.is_cuda or rows.get_device() != torch.cuda.current_device():
+    if not rows.is_cuda or rows.get_device() != _current_device():
         raise ValueError("rows must be on the current CUDA device")
-    stride = seq if p.B > 1 else n * p.d
     _check(lib().mxfp4_cache_write(
-        C.byref(p), rows.data_ptr(), stride, n,
-        _need(first_entry, "first_entry", torch.int64, p.B),
-        _need(count, "count", torch.int64, p.B),
-        _need_cache(p, kv4), kv4.shape[1], _status(dev_status),
+        C.byref(p), rows.data_ptr(), seq if B > 1 else n * d, n,
+        _need(first_entry, "first_entry", torch.int64, B), _need(count, "count", torch.int64, B),
+        _need(kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N, _status(dev_status),
         _raw_stream(stream)))
 
 
@@ -572,13 +574,12 @@ def mxfp4_cache_read(p, kv4, rows, idx=None, first_entry=None, count=None, dev_s
                      stream=None):
     """The values of entries idx[b, i] (int32, -1 skipped) or first_entry[b] + i,
     i < count[b], of kv4 into rows [B, n, d] (bf16)."""
-    rp = _need(rows, "rows", torch.bfloat16, p.B, _size(rows, "rows", 1), p.d)
-    n = rows.shape[1]
+    B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
+    out = _need(rows, "rows", torch.bfloat16, B, n, d)
     _check(lib().mxfp4_cache_read(
-        C.byref(p), _need_cache(p, kv4), kv4.shape[1], _need(idx, "idx", torch.int32, p.B, n),
-        _need(first_entry, "first_entry", torch.int64, p.B),
-        _need(count, "count", torch.int64, p.B),
-        n, rp, _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need(kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N,
+        _need(idx, "idx", torch.int32, B, n), _need(first_entry, "first_entry", torch.int64, B),
+        _need(count, "count", torch.int64, B), n, out, _status(dev_status), _raw_stream(stream)))
 
 
 def _pool_args(p, w_s, b_pos, gamma):
