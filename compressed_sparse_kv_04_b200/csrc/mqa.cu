@@ -950,19 +950,12 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
 #pragma unroll 1
             for (int u = 0; u < X::kU; ++u) {
               const uint32_t w[4] = {cd[0].x, cd[0].y, cd[0].z, cd[0].w};
-              const uint32_t lo = mx_f16_lo(sc[0]);
-              const bool wide = __any_sync(0xffffffffu, sc[0] > 128u);
+              const uint32_t scale = mx_f16_scale(sc[0]);
+              if (sc[0] > kMxF16Top && sc[0] != 255u) report(p.status, CSA_ERR_UNSUPPORTED_SHAPE);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t o[4];
-                mx_values8_f16(w[j], lo, o);
-                if (wide) {
-                  const uint32_t hi = mx_f16_hi(sc[0]);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[i] = mul_f16x2(o[i], hi);
-                  if (sc[0] > kMxF16Top && sc[0] != 255u)
-                    report(p.status, CSA_ERR_UNSUPPORTED_SHAPE);
-                }
+                mx_values8_f16(w[j], scale, o);
                 *reinterpret_cast<uint4*>(unit[j]) = make_uint4(o[0], o[1], o[2], o[3]);
                 unit[j] += X::kStep * 128;
               }

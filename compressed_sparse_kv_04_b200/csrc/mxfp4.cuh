@@ -93,32 +93,32 @@ CSA_DEV void mx_values8(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
   }
 }
 
-// The same in fp16, the form the attention's tensor cores take: a code's
-// exponent and mantissa bits at bits 11..9 of an fp16 are its magnitude times
-// 2^-14, so the factor is 2^(s-113): one product for s <= 128 (scales below
-// 2^-24 / 2^-14 vanish), a second factor 2^(s-128) up to s = 140 (values up
-// to 49152).  Above that (and for 255) the values are NaN.
+// The same in fp16, the form the attention's tensor cores take.  fp16 holds the
+// codes and the factor 2^(s-127) of scale bytes 103 .. 142 (2^-24 .. 2^15): one
+// conversion and one exact product a pair.  Values are exact from s = 104 to
+// s = 140 (49152); a scale below 103 is zero; above 140 it overflows to
+// infinity or NaN (255: NaN), which the caller reports.
 constexpr uint32_t kMxF16Top = 140u;
-CSA_DEV uint32_t mx_f16_lo(uint32_t s) {
-  const float f = __uint_as_float((min(s, 128u) + 14u) << 23);  // 2^(min(s, 128) - 113)
+CSA_DEV uint32_t mx_f16_scale(uint32_t s) {
+  const float f = __uint_as_float(s << 23);  // 2^(s-127); 0 for s = 0, infinity for 255
   return h2_bits(__floats2half2_rn(f, f));
-}
-CSA_DEV uint32_t mx_f16_hi(uint32_t s) {
-  return (s > kMxF16Top ? 0x7E00u : (max(s, 128u) - 113u) << 10) * 0x10001u;
 }
 CSA_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-CSA_DEV void mx_values8_f16(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
-  const uint32_t v = w << 4;
+CSA_DEV void mx_values8_f16(uint32_t w, uint32_t scale, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t sel = (uint32_t)(i | (i << 4) | ((i + 4) << 8) | ((i + 4) << 12));
-    const uint32_t r = __byte_perm(v, w, sel);
-    o[i] = mul_f16x2((r & 0x80008000u) | ((r >> 3) & 0x0E000E00u), lo);
-  }
+  for (int i = 0; i < 4; ++i) o[i] = mul_f16x2(o[i], scale);
 }
 
 }  // namespace csa
