@@ -888,17 +888,16 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       // MXFP4 entries: a thread holds whole blocks of 32 values (16 bytes of
       // codes and their scale byte), fetched one tile ahead straight into
       // registers; their fp16 values go into the stage (exact from scale
-      // 2^-23 on).  Every operand of these products is fp16 (queries,
-      // weights P and window tokens too), not bf16: its three more bits take
-      // the error against 64 bits from 2.7e-3 .. 3.4e-3 (relative, L2) to the
-      // 1.7e-3 that rounding the output to bf16 alone costs, in the same
-      // time, and normalised rows fit its range.  64 rows are
-      // 17 KB against 64 KB of bf16.  The conversion takes about five
-      // instructions a pair of values; its loop stays rolled (one block a
-      // turn, the registers shifted down), since the unrolled one waited on
-      // the instruction cache four issue slots out of five, and eight warps
-      // share it (8 sequences of 8192 entries: 81 us unrolled on four warps,
-      // 54 rolled, 47 on eight warps; 43 without the conversion).
+      // 2^-23 on).  64 rows are 17 KB against 64 KB of bf16.
+      // Every operand of these products is fp16 (queries, weights P and window
+      // tokens too), not bf16: its three more bits take the error against 64
+      // bits from 2.7e-3 .. 3.4e-3 (relative, L2) to the 1.7e-3 that rounding
+      // the output to bf16 alone costs, in the same time, and normalised rows
+      // fit its range.
+      // The conversion competes with the softmax for issue slots and the
+      // instruction cache: 8 sequences of 8192 entries took 81 us with 21
+      // instructions a word of 8 codes on four warps, 47 on eight, 41 with the
+      // hardware's E2M1 conversion (about 10 a word); 39.5 from a bf16 cache.
       using X = MxTile<D>;
       const X x(tid);
       const uint8_t* seq = p.kv4 + (int64_t)b * p.N_cap * mx_row_bytes(D);
@@ -947,22 +946,17 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
             uint8_t* unit[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) unit[j] = at + tile_off(x.row, kMxBlock * x.blk + 8 * j);
-#pragma unroll 1
+#pragma unroll
             for (int u = 0; u < X::kU; ++u) {
-              const uint32_t w[4] = {cd[0].x, cd[0].y, cd[0].z, cd[0].w};
-              const uint32_t scale = mx_f16_scale(sc[0]);
-              if (sc[0] > kMxF16Top && sc[0] != 255u) report(p.status, CSA_ERR_UNSUPPORTED_SHAPE);
+              const uint32_t w[4] = {cd[u].x, cd[u].y, cd[u].z, cd[u].w};
+              const uint32_t scale = mx_f16_scale(sc[u]);
+              if (sc[u] > kMxF16Top && sc[u] != 255u) report(p.status, CSA_ERR_UNSUPPORTED_SHAPE);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t o[4];
                 mx_values8_f16(w[j], scale, o);
-                *reinterpret_cast<uint4*>(unit[j]) = make_uint4(o[0], o[1], o[2], o[3]);
-                unit[j] += X::kStep * 128;
-              }
-#pragma unroll
-              for (int i = 0; i + 1 < X::kU; ++i) {
-                cd[i] = cd[i + 1];
-                sc[i] = sc[i + 1];
+                *reinterpret_cast<uint4*>(unit[j] + u * (X::kStep * 128)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
               }
             }
             fence_proxy_async_smem();

@@ -515,9 +515,10 @@ csa_status mxfp4_cache_read(const csa_params* p, const void* kv4, int64_t N_cap,
  *     bf16.  The products take fp16 operands (query, entries, window rows and
  *     weights each rounded once, to 11 bits, where the calls on bf16 caches
  *     round to 8), which normalised rows fit: entries with a scale byte of
- *     104 .. 140 (2^-23 .. 2^13) are exact, smaller ones round to multiples
- *     of 2^-24, and a larger one is reported (CSA_ERR_UNSUPPORTED_SHAPE in
- *     dev_status) and counts as NaN.  Gains up to 2048 in magnitude fit.
+ *     104 .. 140 (2^-23 .. 2^13) are exact, those with 103 round to multiples
+ *     of 2^-24, smaller ones are zeros, and a larger one is reported
+ *     (CSA_ERR_UNSUPPORTED_SHAPE in dev_status) and makes its row's outputs
+ *     infinite or NaN.  Gains up to 2048 in magnitude fit.
  *   - An entry that is NaN and is selected (or visible, dense) makes its
  *     row's outputs NaN; entries that are not selected are never read.
  *   - The indexer's keys are the E4M3 keys of the bf16 cache.
