@@ -562,6 +562,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tma_load_2d_pair(sc + 4 * kScaleTile, &map_ws, &full[s], 0, ws_row1 + 2 * c);
         }
       }
+      // The MMAs' last arrivals on `empty` come from the even CTA: they land
+      // before this CTA leaves.
+      for (int j = it - C::kStages > 0 ? it - C::kStages : 0; ok && j < it; ++j)
+        ok = mbar_wait(&empty[j % C::kStages], (j / C::kStages) & 1, p.status, abort_flag);
       if (*abort_flag) {  // copies still in flight land before the CTA exits
         if (rank == 0)
           for (int j = it - C::kStages > 0 ? it - C::kStages : 0; j < it; ++j)

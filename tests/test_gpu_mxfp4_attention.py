@@ -252,6 +252,40 @@ def test_repeated_index_counts_twice(orc):
     c.check(orc)
 
 
+def test_entries_past_four_gigabytes():
+    """A cache longer than 2^32 bytes: entries at its end, written, read back and
+    attended to, as in a short cache."""
+    d, N, n = 512, 16_000_000, 96
+    short = Case(1, d, 16, 64, 0, 1, [n - 1], n, k=n, seed=7)
+    p = binding.make_params(1, d, H=16, k=n, window=0, rope_dim=64, m=1)
+    kv4 = binding.mxfp4_cache(p, N)
+    assert kv4.numel() > 2 ** 32
+    rows = short.values()
+    first = torch.tensor([N - n], device=DEV)
+    binding.mxfp4_cache_write(p, rows, kv4, first_entry=first)
+    # (Not the short cache's bytes: a block whose largest stored value is 3 * 2^e
+    # fits the scale 2^(e-1) exactly, so quantising it again halves the scale.)
+    assert np.array_equal(kv4[0, N - n:].cpu().numpy(), mxref.cache_rows(mxref.bf16_values(rows[0])))
+    back = torch.empty_like(rows)
+    binding.mxfp4_cache_read(p, kv4, back, idx=(N - n + torch.arange(
+        n, device=DEV, dtype=torch.int32)).view(1, n))
+    assert torch.equal(back, rows)
+    # (Without rotation, since the query's goes by its position.)
+    p0 = binding.make_params(1, d, H=16, k=n, window=0, rope_dim=0, m=1)
+    ws = binding.workspace(p0, binding.OP_SPARSE_MQA, 1, N)
+    outs = []
+    for cache, pos, sel in ((short.kv4, n - 1, torch.arange(n)), (kv4, N - 1,
+                                                                  N - n + torch.arange(n))):
+        out = torch.empty(1, 16, d, dtype=torch.bfloat16, device=DEV)
+        binding.sparse_mqa_decode_mxfp4(p0, short.q, torch.tensor([pos], device=DEV), cache,
+                                        sel.int().view(1, n).to(DEV),
+                                        torch.tensor([n], dtype=torch.int32, device=DEV),
+                                        short.kv_tok, short.sink, out, ws=ws)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+
+
 def test_two_streams_two_workspaces():
     """Two calls at once, each with its own workspace, repeat each other."""
     a = Case(2, 512, 128, 64, 128, 4, [9000, 7000], 2300, k=512, seed=3)

@@ -124,13 +124,12 @@ def test_small(T):
 @pytest.mark.parametrize("H,D,g,d_g,d_model", [
     (2, 128, 1, 256, 128),     # one group, the smallest inner dimension
     (16, 512, 2, 128, 128),    # long inner dimension, few tiles: K splits
-    (12, 512, 3, 384, 640),    # odd tile counts
+    (12, 512, 3, 512, 640),    # odd tile counts; 640 = 2.5 tiles of 256
+    (8, 512, 2, 384, 384),     # neither product has whole tiles of 256
     (64, 512, 16, 512, 5120),
 ])
 @pytest.mark.parametrize("T", [5, 130, 520])
 def test_shapes(H, D, g, d_g, d_model, T):
-    if g * d_g % 256:
-        d_g = 512
     m = Layer(H, D, g, d_g, d_model, 7)
     o = m.tokens(T)
     y, z = m.run(o)
@@ -214,3 +213,23 @@ def test_rows_behind_the_last_token_are_left():
         torch.cuda.synchronize()
         assert (y[T:] == 7).all() and (z[T:] == 7).all()
         m.check(o, y[:T], z[:T])
+
+
+def test_two_streams_two_workspaces():
+    """Calls of every form at once, each with its own workspace, repeat what
+    they give alone."""
+    m = Layer(64, 512, 8, 1024, 4096, 6)
+    tokens = [m.tokens(T) for T in (8, 200, 700)]
+    alone = [m.run(o, with_y=False)[1] for o in tokens]
+    ws = [torch.empty(binding.grouped_out_proj_mxfp4_workspace_bytes(o.shape[0], 64, 512, 8, 1024,
+                                                                     4096),
+                      dtype=torch.uint8, device=DEV) for o in tokens]
+    z = [torch.empty_like(a) for a in alone]
+    streams = [torch.cuda.Stream() for _ in tokens]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o, w, out, s in zip(tokens, ws, z, streams):
+            binding.grouped_out_proj_mxfp4(o, m.w_g, m.w_gs, m.w_o, m.w_os, out, ws=w, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, z):
+        assert torch.equal(a, b)
