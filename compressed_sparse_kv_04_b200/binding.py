@@ -478,9 +478,15 @@ def mxfp4_cache(p, N_cap, device=None):
 
 _ROW_BYTES = {}
 _Tensor = torch.Tensor
-# (None in a torch built without CUDA: only CUDA tensors reach them.)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device():
+    """The current CUDA device, which every tensor of a call has to be on; -2
+    (no tensor's device) where there is none."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return -2
 
 
 def _row_bytes(d):
@@ -490,14 +496,14 @@ def _row_bytes(d):
     return n
 
 
-def _need(t, name, dtype, *shape):
+def _need(dev, t, name, dtype, *shape):
     """Address of a tensor that must have this dtype and shape (None: any
     length), be contiguous and sit on the current device; None passes."""
     if t is None:
         return None
     # The usual case in few steps: a decode step makes a dozen of these checks.
     if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
-            t.is_cuda and t.get_device() == _current_device()):
+            t.get_device() == dev):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
@@ -505,7 +511,7 @@ def _need(t, name, dtype, *shape):
             n is not None and n != m for n, m in zip(shape, t.shape)):
         want = ", ".join("*" if n is None else str(n) for n in shape)
         raise ValueError(f"{name} must be {dtype} [{want}], not {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -521,29 +527,30 @@ def _size(t, name, dim):
     return t.size(dim)
 
 
-def _need_cache(p, kv4):
-    return _need(kv4, "kv4", torch.uint8, p.B, _size(kv4, "kv4", 1), _row_bytes(p.d))
+def _need_cache(dev, p, kv4):
+    return _need(dev, kv4, "kv4", torch.uint8, p.B, _size(kv4, "kv4", 1), _row_bytes(p.d))
 
 
-def _need_tok(p, kv_tok):
-    return _need(kv_tok, "kv_tok", torch.bfloat16, p.B, _size(kv_tok, "kv_tok", 1), p.d)
+def _need_tok(dev, p, kv_tok):
+    return _need(dev, kv_tok, "kv_tok", torch.bfloat16, p.B, _size(kv_tok, "kv_tok", 1), p.d)
 
 
-def _status(dev_status):
-    return None if dev_status is None else _need(dev_status, "dev_status", torch.int32, 1)
+def _status(dev, dev_status):
+    return None if dev_status is None else _need(dev, dev_status, "dev_status", torch.int32, 1)
 
 
-def _raw_stream(stream):
+def _raw_stream(dev, stream):
     if stream is not None:
         return stream.cuda_stream
-    return _current_stream(_current_device())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _is_mxfp4(p, kv_c, kv_tok):
+    dev = _device()
     if kv_c.dtype != torch.uint8:
         return False
-    _need_cache(p, kv_c)
-    _need_tok(p, kv_tok)
+    _need_cache(dev, p, kv_c)
+    _need_tok(dev, p, kv_tok)
     return True
 
 
@@ -554,6 +561,7 @@ def _ws(ws):
 def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
     """Quantises rows [B, n, d] (bf16; each sequence's rows contiguous) into
     entries first_entry[b] + i, i < count[b], of kv4."""
+    dev = _device()
     B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
     if rows.dtype is not torch.bfloat16 or rows.shape != (B, n, d):
         raise ValueError(f"rows must be bfloat16 [{B}, n, {d}], not {rows.dtype} "
@@ -561,94 +569,107 @@ def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=Non
     seq, row, one = rows.stride()
     if n and (one != 1 or (n > 1 and row != d)):
         raise ValueError("each sequence's rows must be contiguous")
-    if not rows.is_cuda or rows.get_device() != _current_device():
+    if rows.get_device() != dev:
         raise ValueError("rows must be on the current CUDA device")
     _check(lib().mxfp4_cache_write(
         C.byref(p), rows.data_ptr(), seq if B > 1 else n * d, n,
-        _need(first_entry, "first_entry", torch.int64, B), _need(count, "count", torch.int64, B),
-        _need(kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N, _status(dev_status),
-        _raw_stream(stream)))
+        _need(dev, first_entry, "first_entry", torch.int64, B),
+        _need(dev, count, "count", torch.int64, B),
+        _need(dev, kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N, _status(dev, dev_status),
+        _raw_stream(dev, stream)))
 
 
 def mxfp4_cache_read(p, kv4, rows, idx=None, first_entry=None, count=None, dev_status=None,
                      stream=None):
     """The values of entries idx[b, i] (int32, -1 skipped) or first_entry[b] + i,
     i < count[b], of kv4 into rows [B, n, d] (bf16)."""
+    dev = _device()
     B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
-    out = _need(rows, "rows", torch.bfloat16, B, n, d)
+    out = _need(dev, rows, "rows", torch.bfloat16, B, n, d)
     _check(lib().mxfp4_cache_read(
-        C.byref(p), _need(kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N,
-        _need(idx, "idx", torch.int32, B, n), _need(first_entry, "first_entry", torch.int64, B),
-        _need(count, "count", torch.int64, B), n, out, _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need(dev, kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N,
+        _need(dev, idx, "idx", torch.int32, B, n),
+        _need(dev, first_entry, "first_entry", torch.int64, B),
+        _need(dev, count, "count", torch.int64, B), n, out, _status(dev, dev_status),
+        _raw_stream(dev, stream)))
 
 
-def _pool_args(p, w_s, b_pos, gamma):
+def _pool_args(dev, p, w_s, b_pos, gamma):
     f32 = torch.float32
-    return (_need(w_s, "w_s", f32, p.d), _need(b_pos, "b_pos", f32, p.m + p.overlap),
-            _need(gamma, "gamma", f32, p.d))
+    return (_need(dev, w_s, "w_s", f32, p.d), _need(dev, b_pos, "b_pos", f32, p.m + p.overlap),
+            _need(dev, gamma, "gamma", f32, p.d))
 
 
-def _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L_cap, N_cap):
+def _index_pool_args(dev, p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L_cap, N_cap):
     f32 = torch.float32
-    return (_need(idx_tok, "idx_tok", torch.bfloat16, p.B, L_cap, p.D_I),
-            _need(w_s_idx, "w_s_idx", f32, p.D_I),
-            _need(b_pos_idx, "b_pos_idx", f32, p.m + p.overlap),
-            _need(idx_key, "idx_key", torch.uint8, p.B, N_cap, p.D_I),
-            _need(idx_scale, "idx_scale", f32, p.B, N_cap))
+    return (_need(dev, idx_tok, "idx_tok", torch.bfloat16, p.B, L_cap, p.D_I),
+            _need(dev, w_s_idx, "w_s_idx", f32, p.D_I),
+            _need(dev, b_pos_idx, "b_pos_idx", f32, p.m + p.overlap),
+            _need(dev, idx_key, "idx_key", torch.uint8, p.B, N_cap, p.D_I),
+            _need(dev, idx_scale, "idx_scale", f32, p.B, N_cap))
 
 
 def hca_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv4,
                        dev_status=None, stream=None):
     """hca_compress into a 4-bit cache."""
+    dev = _device()
     _check(lib().hca_compress_mxfp4(
-        C.byref(p), _need_tok(p, kv_tok), kv_tok.shape[1],
-        _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
-        n_blocks, _need_cache(p, kv4), kv4.shape[1], _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need_tok(dev, p, kv_tok), kv_tok.shape[1],
+        _need(dev, ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(dev, p, w_s, b_pos, gamma),
+        first_block,
+        n_blocks, _need_cache(dev, p, kv4), kv4.shape[1], _status(dev, dev_status),
+        _raw_stream(dev, stream)))
 
 
 def csa_compress_mxfp4(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv4,
                        idx_tok=None, w_s_idx=None, b_pos_idx=None, idx_key=None, idx_scale=None,
                        dev_status=None, stream=None):
     """csa_compress into a 4-bit cache (indexer keys as csa_compress)."""
+    dev = _device()
     L, N = kv_tok.shape[1], kv4.shape[1]
     _check(lib().csa_compress_mxfp4(
-        C.byref(p), _need_tok(p, kv_tok), L,
-        _need(ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(p, w_s, b_pos, gamma), first_block,
-        n_blocks, _need_cache(p, kv4), N,
-        *_index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L, N),
-        _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need_tok(dev, p, kv_tok), L,
+        _need(dev, ctx_len, "ctx_len", torch.int64, p.B), *_pool_args(dev, p, w_s, b_pos, gamma),
+        first_block,
+        n_blocks, _need_cache(dev, p, kv4), N,
+        *_index_pool_args(dev, p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L, N),
+        _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
-def _mqa_inputs(p, rows, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse):
+def _mqa_inputs(dev, p, rows, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse):
     """Checked pointers of the attention's tensors, `rows` queries."""
     bf, f32 = torch.bfloat16, torch.float32
-    return dict(q=_need(q, "q", bf, rows, p.H, p.d), kv4=_need_cache(p, kv4),
-                kv_tok=_need_tok(p, kv_tok),
-                sink=_need(sink, "sink", f32, p.H), gq=_need(gamma_q, "gamma_q", f32, p.d),
-                gkv=_need(gamma_kv, "gamma_kv", f32, p.d),
-                out=_need(out, "out", bf, rows, p.H, p.d),
-                lse=_need(lse, "lse", f32, rows, p.H))
+    return dict(q=_need(dev, q, "q", bf, rows, p.H, p.d), kv4=_need_cache(dev, p, kv4),
+                kv_tok=_need_tok(dev, p, kv_tok),
+                sink=_need(dev, sink, "sink", f32, p.H),
+                gq=_need(dev, gamma_q, "gamma_q", f32, p.d),
+                gkv=_need(dev, gamma_kv, "gamma_kv", f32, p.d),
+                out=_need(dev, out, "out", bf, rows, p.H, p.d),
+                lse=_need(dev, lse, "lse", f32, rows, p.H))
 
 
 def sparse_mqa_decode_mxfp4(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink, out, gamma_q=None,
                             gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
     """sparse_mqa_decode over a 4-bit cache."""
-    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    dev = _device()
+    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     _check(lib().sparse_mqa_decode_mxfp4(
-        C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
-        _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
-        _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
-        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev_status), _raw_stream(stream)))
+        C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
+        _need(dev, topk_idx, "topk_idx", torch.int32, p.B, p.k),
+        _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
+        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev, dev_status),
+        _raw_stream(dev, stream)))
 
 
 def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, gamma_kv=None,
                            lse=None, ws=None, dev_status=None, stream=None):
     """dense_mqa_decode over a 4-bit cache."""
-    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    dev = _device()
+    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     _check(lib().dense_mqa_decode_mxfp4(
-        C.byref(p), a["q"], _need(pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
+        C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
         a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
-        _status(dev_status), _raw_stream(stream)))
+        _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
@@ -656,27 +677,33 @@ def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx
                             out, gamma_q=None, gamma_kv=None, ws=None, dev_status=None,
                             stream=None):
     """csa_prefill_chunk on a 4-bit cache (B = 1)."""
-    a = _mqa_inputs(p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, None)
+    dev = _device()
+    a = _mqa_inputs(dev, p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, None)
     L, N = kv_tok.shape[1], kv4.shape[1]
-    it, wsi, bpi, ik, isc = _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L,
-                                             N)
+    it, wsi, bpi, ik, isc = _index_pool_args(dev, p, idx_tok, w_s_idx, b_pos_idx, idx_key,
+                                             idx_scale, L, N)
     _check(lib().csa_prefill_chunk_mxfp4(
-        C.byref(p), P, T, a["kv_tok"], it, L, *_pool_args(p, w_s, b_pos, gamma), wsi, bpi, a["kv4"],
-        ik, isc, N, a["q"], _need(q_idx, "q_idx", torch.uint8, T, p.H_I, p.D_I),
-        _need(q_scale, "q_scale", torch.float32, T, p.H_I), _need(w, "w", torch.float32, T, p.H_I),
-        a["sink"], a["gq"], a["gkv"], _need(topk_idx, "topk_idx", torch.int32, T, p.k),
-        _need(topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws), _status(dev_status),
-        _raw_stream(stream)))
+        C.byref(p), P, T, a["kv_tok"], it, L, *_pool_args(dev, p, w_s, b_pos, gamma), wsi, bpi,
+        a["kv4"],
+        ik, isc, N, a["q"], _need(dev, q_idx, "q_idx", torch.uint8, T, p.H_I, p.D_I),
+        _need(dev, q_scale, "q_scale", torch.float32, T, p.H_I),
+        _need(dev, w, "w", torch.float32, T, p.H_I),
+        a["sink"], a["gq"], a["gkv"], _need(dev, topk_idx, "topk_idx", torch.int32, T, p.k),
+        _need(dev, topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws),
+        _status(dev, dev_status),
+        _raw_stream(dev, stream)))
 
 
 def hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
                             gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
     """hca_prefill_chunk on a 4-bit cache (B = 1)."""
-    a = _mqa_inputs(p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    dev = _device()
+    a = _mqa_inputs(dev, p, T, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     _check(lib().hca_prefill_chunk_mxfp4(
-        C.byref(p), P, T, a["kv_tok"], kv_tok.shape[1], *_pool_args(p, w_s, b_pos, gamma), a["kv4"],
+        C.byref(p), P, T, a["kv_tok"], kv_tok.shape[1], *_pool_args(dev, p, w_s, b_pos, gamma),
+        a["kv4"],
         kv4.shape[1], a["q"], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
-        _status(dev_status), _raw_stream(stream)))
+        _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,
@@ -684,29 +711,31 @@ def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx,
                           gamma_q=None, gamma_kv=None, lse=None, ws=None, dev_status=None,
                           stream=None):
     """csa_decode_step on a 4-bit cache."""
-    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    dev = _device()
+    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     L, N = kv_tok.shape[1], kv4.shape[1]
-    it, wsi, bpi, ik, isc = _index_pool_args(p, idx_tok, w_s_idx, b_pos_idx, idx_key, idx_scale, L,
-                                             N)
+    it, wsi, bpi, ik, isc = _index_pool_args(dev, p, idx_tok, w_s_idx, b_pos_idx, idx_key,
+                                             idx_scale, L, N)
     _check(lib().csa_decode_step_mxfp4(
-        C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], it, L,
-        *_pool_args(p, w_s, b_pos, gamma), wsi, bpi, a["kv4"], ik, isc, N, a["q"],
-        _need(q_idx, "q_idx", torch.uint8, p.B, p.H_I, p.D_I),
-        _need(q_scale, "q_scale", torch.float32, p.B, p.H_I),
-        _need(w, "w", torch.float32, p.B, p.H_I), a["sink"], a["gq"], a["gkv"],
-        _need(topk_idx, "topk_idx", torch.int32, p.B, p.k),
-        _need(topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(ws),
-        _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], it, L,
+        *_pool_args(dev, p, w_s, b_pos, gamma), wsi, bpi, a["kv4"], ik, isc, N, a["q"],
+        _need(dev, q_idx, "q_idx", torch.uint8, p.B, p.H_I, p.D_I),
+        _need(dev, q_scale, "q_scale", torch.float32, p.B, p.H_I),
+        _need(dev, w, "w", torch.float32, p.B, p.H_I), a["sink"], a["gq"], a["gkv"],
+        _need(dev, topk_idx, "topk_idx", torch.int32, p.B, p.k),
+        _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(ws),
+        _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out, gamma_q=None,
                           gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
     """hca_decode_step on a 4-bit cache."""
-    a = _mqa_inputs(p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
+    dev = _device()
+    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     _check(lib().hca_decode_step_mxfp4(
-        C.byref(p), _need(pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
-        *_pool_args(p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
-        a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev_status), _raw_stream(stream)))
+        C.byref(p), _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
+        *_pool_args(dev, p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
+        a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 def mxfp4_scale_bytes(rows, cols):
@@ -720,6 +749,7 @@ def mxfp4_scale_bytes(rows, cols):
 def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     """x [rows, cols] (bf16, each row contiguous) as an operand of the 4-bit
     product: (codes [rows, cols/2], scale tiles), allocated when not given."""
+    dev = _device()
     rows, cols = _size(x, "x", 0), _size(x, "x", 1)
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or \
             x.get_device() != torch.cuda.current_device():
@@ -731,16 +761,16 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     if scales is None:
         scales = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check(lib().mxfp4_quantize(rows, cols, x.data_ptr(), x.stride(0) if rows > 1 else cols,
-                                _need(codes, "codes", torch.uint8, rows, cols // 2),
-                                _need_scales(scales, "scales", n), _raw_stream(stream)))
+                                _need(dev, codes, "codes", torch.uint8, rows, cols // 2),
+                                _need_scales(dev, scales, "scales", n), _raw_stream(dev, stream)))
     return codes, scales
 
 
-def _need_scales(t, name, n):
+def _need_scales(dev, t, name, n):
     """Scale tiles: `n` bytes in any shape."""
     if isinstance(t, torch.Tensor) and t.numel() != n:
         raise ValueError(f"{name} must hold {n} bytes, not {t.numel()}")
-    return _need(t, name, torch.uint8, *(t.shape if isinstance(t, torch.Tensor) else ()))
+    return _need(dev, t, name, torch.uint8, *(t.shape if isinstance(t, torch.Tensor) else ()))
 
 
 def grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model):
@@ -755,6 +785,7 @@ def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None
     """grouped_out_proj with 4-bit weights and activations: o [T, H, D] bf16,
     w_g [g, d_g, H/g*D/2] and w_o [d_model, g*d_g/2] codes with their scale
     tiles (mxfp4_quantize).  The workspace is allocated here when not given."""
+    dev = _device()
     if not isinstance(o, torch.Tensor) or o.dim() != 3:
         raise ValueError("o must be [T, H, D]")
     T, H, D = o.shape
@@ -766,12 +797,13 @@ def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None
     k1, k2 = H // max(g, 1) * D, g * d_g
     u8, bf = torch.uint8, torch.bfloat16
     _check(lib().grouped_out_proj_mxfp4(
-        T, H, D, g, d_g, d_model, _need(o, "o", bf, T, H, D), _need(w_g, "w_g", u8, g, d_g, k1 // 2),
-        _need_scales(w_g_scale, "w_g_scale", -(-k2 // 128) * (k1 // 128) * 512),
-        _need(w_o, "w_o", u8, d_model, k2 // 2),
-        _need_scales(w_o_scale, "w_o_scale", -(-d_model // 128) * (k2 // 128) * 512),
-        _need(y, "y", bf, T, k2), _need(z, "z", bf, T, d_model), _ptr(ws), ws.nbytes,
-        _status(dev_status), _raw_stream(stream)))
+        T, H, D, g, d_g, d_model, _need(dev, o, "o", bf, T, H, D),
+        _need(dev, w_g, "w_g", u8, g, d_g, k1 // 2),
+        _need_scales(dev, w_g_scale, "w_g_scale", -(-k2 // 128) * (k1 // 128) * 512),
+        _need(dev, w_o, "w_o", u8, d_model, k2 // 2),
+        _need_scales(dev, w_o_scale, "w_o_scale", -(-d_model // 128) * (k2 // 128) * 512),
+        _need(dev, y, "y", bf, T, k2), _need(dev, z, "z", bf, T, d_model), _ptr(ws), ws.nbytes,
+        _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 # ------------------------------------------- context split over several devices --
