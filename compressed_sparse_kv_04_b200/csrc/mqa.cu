@@ -80,6 +80,13 @@ constexpr int kTransform = kMx ? 256 : 128;
 template <bool kMx>
 constexpr int kBlockThreads = kThreads - 128 + kTransform<kMx>;
 constexpr float kRescaleThreshold = 8.0f;
+// Weights are 2^(logit - m) with m this far (log2) below the running maximum.
+// In fp16 (MXFP4 caches) the largest is then 2^4, at most 2^15.6 before O is
+// rescaled, and a weight is rounded by at most 2^-29 of the row's largest (by
+// 2^-25 with m at the maximum: a long list of weights that small would lose
+// its share of the output).  bf16 has fp32's range.
+template <bool kMx>
+constexpr float kWeightBias = kMx ? 4.0f : 0.0f;
 
 template <int D>
 struct MCfg {
@@ -1145,8 +1152,9 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));  // the row's other half
       // Online softmax with lazy rescaling.
-      const bool grow = mt > m_run + kRescaleThreshold * 1.4426950408889634f || m_run == -INFINITY;
-      const float m_new = grow ? fmaxf(mt, m_run) : m_run;
+      constexpr float kGrow = kRescaleThreshold * 1.4426950408889634f + kWeightBias<kMx>;
+      const bool grow = mt > m_run + kGrow || m_run == -INFINITY;
+      const float m_new = grow ? fmaxf(kMx ? mt - kWeightBias<kMx> : mt, m_run) : m_run;
       const bool need = grow && m_run != -INFINITY;
       // P buffer a was last read by P.V of tile it-2; rescaling O needs
       // every earlier P.V complete (the latest is tile it-1).  pvdone[x]
@@ -1390,7 +1398,7 @@ int clusters_resident(const void* kern, int variant, int threads, int S, size_t 
   if (ok) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S, 1, 1);
-      cfg.blockDim = dim3(threads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -160,6 +160,45 @@ def test_large_and_small_scales(orc, k):
     Case(2, 512, 20, 64, 128, 4, [900, 800], 230, k=k, scale=2.0 ** -12).check(orc)
 
 
+@pytest.mark.parametrize("k", [0, 64])
+def test_many_small_weights_beside_a_large_one(k):
+    """63 entries with weights of 2^-25.2 of the row's largest: together they are
+    all of the output's dims 32 .. (the largest weight's entry is zero there).
+
+    qhat is about sqrt(128) in dim 0, so a logit is the entry's dim 0.  Each weight is
+    off by at most 2^-29 of the largest and by its logits' rounding (17.5 times
+    2^-11), the sum by the output's 2^-8."""
+    B = torch.cuda.get_device_properties(0).multi_processor_count  # one split per row
+    N = 64
+    p = binding.make_params(B, 128, H=2, k=k, window=0, rope_dim=0, m=4)
+    rows = torch.zeros(B, N, 128, dtype=torch.bfloat16, device=DEV)
+    rows[:, :, 0] = -1.5
+    rows[:, :, 32:] = 1.0
+    rows[:, 7] = 0.0
+    rows[:, 7, 0] = 16.0
+    kv4 = binding.mxfp4_cache(p, N)
+    binding.mxfp4_cache_write(p, rows, kv4)
+    q = torch.zeros(B, 2, 128, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1.0
+    pos = torch.full((B,), 4 * N - 1, dtype=torch.int64, device=DEV)
+    kv_tok = torch.zeros(B, 4 * N, 128, dtype=torch.bfloat16, device=DEV)
+    sink = torch.full((2,), float("-inf"), device=DEV)
+    out = torch.full((B, 2, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = binding.workspace(p, binding.OP_SPARSE_MQA if k else binding.OP_DENSE_MQA, 1, N)
+    if k:
+        sel = torch.arange(N, dtype=torch.int32, device=DEV).repeat(B, 1)
+        cnt = torch.full((B,), N, dtype=torch.int32, device=DEV)
+        binding.sparse_mqa_decode_mxfp4(p, q, pos, kv4, sel, cnt, kv_tok, sink, out, ws=ws)
+    else:
+        binding.dense_mqa_decode_mxfp4(p, q, pos, kv4, kv_tok, sink, out, ws=ws)
+    small = np.exp(-17.5 / np.sqrt(1 + 128 * p.eps))
+    want = 63 * small / (1 + 63 * small)
+    tol = want * (2.0 ** -29 / small + 17.5 * 2.0 ** -11 + 2.0 ** -8)
+    got = out[:, :, 32:].double()
+    assert (got - want).abs().max().item() <= tol
+    assert (out[:, :, 0].double() - 16).abs().max().item() <= 16 * 2.0 ** -8
+
+
 @pytest.mark.parametrize("k", [0, 100])
 def test_scales_outside_fp16(orc, k):
     """Scale bytes above 140 (values above 49152) are reported and make their
