@@ -554,8 +554,20 @@ def _is_mxfp4(p, kv_c, kv_tok):
     return True
 
 
-def _ws(ws):
-    return _ptr(ws), 0 if ws is None else ws.nbytes
+def _ws(dev, ws):
+    """Address and bytes of a workspace (any type and shape, on the current
+    device)."""
+    if ws is None:
+        return None, 0
+    return _need(dev, ws, "ws", getattr(ws, "dtype", None), *getattr(ws, "shape", ())), ws.nbytes
+
+
+def _empty(dev, stream, *shape):
+    """uint8 memory that belongs to the stream of the call."""
+    if stream is None:
+        return torch.empty(*shape, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=torch.uint8, device=dev)
 
 
 def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
@@ -657,7 +669,7 @@ def sparse_mqa_decode_mxfp4(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink, 
         C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
         _need(dev, topk_idx, "topk_idx", torch.int32, p.B, p.k),
         _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
-        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev, dev_status),
+        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(dev, ws), _status(dev, dev_status),
         _raw_stream(dev, stream)))
 
 
@@ -668,7 +680,7 @@ def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, ga
     a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
     _check(lib().dense_mqa_decode_mxfp4(
         C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
-        a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
+        a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(dev, ws),
         _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
@@ -689,7 +701,7 @@ def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx
         _need(dev, q_scale, "q_scale", torch.float32, T, p.H_I),
         _need(dev, w, "w", torch.float32, T, p.H_I),
         a["sink"], a["gq"], a["gkv"], _need(dev, topk_idx, "topk_idx", torch.int32, T, p.k),
-        _need(dev, topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(ws),
+        _need(dev, topk_cnt, "topk_cnt", torch.int32, T), a["out"], *_ws(dev, ws),
         _status(dev, dev_status),
         _raw_stream(dev, stream)))
 
@@ -702,7 +714,7 @@ def hca_prefill_chunk_mxfp4(p, P, T, kv_tok, w_s, b_pos, gamma, kv4, q, sink, ou
     _check(lib().hca_prefill_chunk_mxfp4(
         C.byref(p), P, T, a["kv_tok"], kv_tok.shape[1], *_pool_args(dev, p, w_s, b_pos, gamma),
         a["kv4"],
-        kv4.shape[1], a["q"], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(ws),
+        kv4.shape[1], a["q"], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(dev, ws),
         _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
@@ -723,7 +735,7 @@ def csa_decode_step_mxfp4(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx,
         _need(dev, q_scale, "q_scale", torch.float32, p.B, p.H_I),
         _need(dev, w, "w", torch.float32, p.B, p.H_I), a["sink"], a["gq"], a["gkv"],
         _need(dev, topk_idx, "topk_idx", torch.int32, p.B, p.k),
-        _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(ws),
+        _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["out"], a["lse"], *_ws(dev, ws),
         _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
@@ -735,7 +747,7 @@ def hca_decode_step_mxfp4(p, pos_q, kv_tok, w_s, b_pos, gamma, kv4, q, sink, out
     _check(lib().hca_decode_step_mxfp4(
         C.byref(p), _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv_tok"], kv_tok.shape[1],
         *_pool_args(dev, p, w_s, b_pos, gamma), a["kv4"], kv4.shape[1], a["q"], a["sink"], a["gq"],
-        a["gkv"], a["out"], a["lse"], *_ws(ws), _status(dev, dev_status), _raw_stream(dev, stream)))
+        a["gkv"], a["out"], a["lse"], *_ws(dev, ws), _status(dev, dev_status), _raw_stream(dev, stream)))
 
 
 def mxfp4_scale_bytes(rows, cols):
@@ -755,11 +767,11 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
             x.get_device() != torch.cuda.current_device():
         raise ValueError("x must be bfloat16 [rows, cols] with contiguous rows, on the current "
                          "CUDA device")
-    n = mxfp4_scale_bytes(rows, cols)
+    n = mxfp4_scale_bytes(rows, cols) if rows else 0
     if codes is None:
-        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        codes = _empty(dev, stream, rows, cols // 2)
     if scales is None:
-        scales = torch.empty(n, dtype=torch.uint8, device=x.device)
+        scales = _empty(dev, stream, n)
     _check(lib().mxfp4_quantize(rows, cols, x.data_ptr(), x.stride(0) if rows > 1 else cols,
                                 _need(dev, codes, "codes", torch.uint8, rows, cols // 2),
                                 _need_scales(dev, scales, "scales", n), _raw_stream(dev, stream)))
@@ -792,8 +804,7 @@ def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None
     g, d_g = _size(w_g, "w_g", 0), _size(w_g, "w_g", 1)
     d_model = _size(w_o, "w_o", 0)
     if ws is None:
-        ws = torch.empty(grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model),
-                         dtype=torch.uint8, device=o.device)
+        ws = _empty(dev, stream, grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model))
     k1, k2 = H // max(g, 1) * D, g * d_g
     u8, bf = torch.uint8, torch.bfloat16
     _check(lib().grouped_out_proj_mxfp4(
@@ -802,7 +813,7 @@ def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None
         _need_scales(dev, w_g_scale, "w_g_scale", -(-k2 // 128) * (k1 // 128) * 512),
         _need(dev, w_o, "w_o", u8, d_model, k2 // 2),
         _need_scales(dev, w_o_scale, "w_o_scale", -(-d_model // 128) * (k2 // 128) * 512),
-        _need(dev, y, "y", bf, T, k2), _need(dev, z, "z", bf, T, d_model), _ptr(ws), ws.nbytes,
+        _need(dev, y, "y", bf, T, k2), _need(dev, z, "z", bf, T, d_model), *_ws(dev, ws),
         _status(dev, dev_status), _raw_stream(dev, stream)))
 
 

@@ -233,3 +233,37 @@ def test_two_streams_two_workspaces():
     torch.cuda.synchronize()
     for a, b in zip(alone, z):
         assert torch.equal(a, b)
+
+
+def test_memory_of_a_call_belongs_to_its_stream():
+    """Operands and workspace that a call on another stream allocates itself:
+    freed and allocated again at once on the current stream, they are not
+    written to before the call has read them."""
+    T, H, D, g, d_g, d_model = 200, 32, 512, 4, 512, 1024
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    o = torch.randn(T, H, D, generator=gen, device=DEV).bfloat16()
+    wg = torch.randn(g * d_g, H // g * D, generator=gen, device=DEV).bfloat16()
+    wo = torch.randn(d_model, g * d_g, generator=gen, device=DEV).bfloat16()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    wgc, wgs = binding.mxfp4_quantize(wg, stream=s)
+    woc, wos = binding.mxfp4_quantize(wo, stream=s)
+    wgc = wgc.view(g, d_g, -1)
+    z = torch.empty(T, d_model, dtype=torch.bfloat16, device=DEV)
+    want = torch.empty_like(z)
+    s.synchronize()
+    binding.grouped_out_proj_mxfp4(o, wgc, wgs, woc, wos, want)
+    torch.cuda.synchronize()
+    n = binding.grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model)
+    for _ in range(20):
+        z.zero_()
+        s.wait_stream(torch.cuda.current_stream())
+        binding.grouped_out_proj_mxfp4(o, wgc, wgs, woc, wos, z, stream=s)
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(z, want)
+
+
+def test_no_rows():
+    codes, scales = binding.mxfp4_quantize(torch.zeros(0, 256, dtype=torch.bfloat16, device=DEV))
+    assert codes.shape == (0, 128) and scales.numel() == 0

@@ -169,3 +169,12 @@ def test_projection_refusals(L):
     assert L.grouped_out_proj_mxfp4(*ok, *p, 8, 1 << 40, None, None) == 1  # misaligned
     with pytest.raises(ValueError):
         binding.grouped_out_proj_mxfp4(torch.zeros(2, 3), None, None, None, None, None)
+
+
+def test_workspace_is_checked_like_every_tensor():
+    """On the host, and of another type: refused before the library sees it."""
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        binding._ws(binding._device(), torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="ws"):
+        binding._ws(binding._device(), 16)
+    assert binding._ws(binding._device(), None) == (None, 0)
