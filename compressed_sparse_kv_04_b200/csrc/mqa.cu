@@ -206,14 +206,16 @@ CSA_DEV bool wait_all(uint64_t* bar, uint32_t parity, const Params& p, volatile 
 // (fp16) and the (max, sum) pair of each split.
 // kLdg: they come from an earlier kernel (read-only path); otherwise they were
 // written during this kernel by other CTAs and are read from L2.
-template <int D, bool kLdg>
+// kParts: warps that share the head's dims (part `part` of them: D / kParts).
+template <int D, int kParts, bool kLdg>
 struct Partials {
   const __half* src;  // split 0's dims of this lane
   const float* ml;    // split 0's maximum of this head
   int64_t stride;     // halves between splits
   int H;
-  CSA_DEV Partials(const Params& p, int row, int h, int lane)
-      : src(p.part_o + ((int64_t)row * p.splits * p.H + h) * D + lane * (D / 32)),
+  CSA_DEV Partials(const Params& p, int row, int h, int part, int lane)
+      : src(p.part_o + ((int64_t)row * p.splits * p.H + h) * D + part * (D / kParts) +
+            lane * (D / kParts / 32)),
         ml(p.part_ml + (int64_t)row * p.splits * 2 * p.H + h), stride((int64_t)p.H * D), H(p.H) {}
   template <typename T>
   CSA_DEV static T ld(const T* a) {
@@ -221,19 +223,19 @@ struct Partials {
   }
   CSA_DEV float maximum(int s) const { return ld(ml + (int64_t)s * 2 * H); }
   CSA_DEV float sum(int s) const { return ld(ml + (int64_t)s * 2 * H + H); }
-  CSA_DEV uint4 load16(int s, int i) const {
-    return ld(reinterpret_cast<const uint4*>(src + (int64_t)s * stride) + i);
+  CSA_DEV uint4 load16(int s) const {
+    return ld(reinterpret_cast<const uint4*>(src + (int64_t)s * stride));
   }
   CSA_DEV uint2 load8(int s) const {
     return ld(reinterpret_cast<const uint2*>(src + (int64_t)s * stride));
   }
 };
 
-// Merge of the split partials of one (row, head) by one warp: fold in the
+// Merge of the split partials of one (row, head) by kParts warps: fold in the
 // sink, normalise, apply the inverse rotation, store bf16 (and the
-// log-sum-exp).  Lane l owns dims [l*VPL, (l+1)*VPL) (VPL = D/32), so the
-// output row leaves as one coalesced 32-lane store and the rotated pairs
-// (d, d + R/2) sit in lanes l and l ^ (R/2/VPL).  The S (max, sum) pairs
+// log-sum-exp).  Lane l owns dims [l*VPL, (l+1)*VPL) of its warp's part (VPL =
+// D/kParts/32), so the output leaves in coalesced 32-lane stores and the rotated
+// pairs (d, d + R/2) sit in lanes l and l ^ (R/2/VPL) of the last part.  The S (max, sum) pairs
 // become one weight per split (wsplit: S floats of this warp's shared
 // memory).  The first G splits' partials are loaded together with the
 // (max, sum) pairs, so that with S <= G the warp waits on one round of L2
@@ -247,21 +249,20 @@ CSA_DEV float2 row_angle(const Params& p, int row, int lane) {
   return make_float2(sn, cs);
 }
 
-template <int D, int R, int G, bool kLdg>
-CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, int lane,
+template <int D, int R, int G, int kParts, bool kLdg>
+CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, int part, int lane,
                         float* wsplit) {
-  const Partials<D, kLdg> src(p, row, h, lane);
-  constexpr int VPL = D / 32;     // dims per lane: 16 (D = 512) or 4 (D = 128)
-  constexpr int NW = VPL / 2;     // 32-bit words (fp16 pairs) per lane and split
-  static_assert(VPL == 16 || VPL == 4, "D must be 512 or 128");
+  const Partials<D, kParts, kLdg> src(p, row, h, part, lane);
+  constexpr int VPL = D / kParts / 32;  // dims per lane: 8 or 4
+  constexpr int NW = VPL / 2;           // 32-bit words (fp16 pairs) per lane and split
+  static_assert(VPL == 8 || VPL == 4, "a lane's dims are one load");
+  static_assert(D / kParts >= R, "the rotated dims belong to one warp");
   const int S = p.splits;
   auto load = [&](int s, uint32_t (&v)[NW]) {
-    if constexpr (VPL == 16) {
-      *reinterpret_cast<uint4*>(&v[0]) = src.load16(s, 0);
-      *reinterpret_cast<uint4*>(&v[4]) = src.load16(s, 1);
-    } else {
+    if constexpr (VPL == 8)
+      *reinterpret_cast<uint4*>(&v[0]) = src.load16(s);
+    else
       *reinterpret_cast<uint2*>(&v[0]) = src.load8(s);
-    }
   };
   uint32_t buf[G][NW];
 #pragma unroll
@@ -293,7 +294,8 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
     if (z2 != -INFINITY) L += exp2f(z2 - M);
   }
   __syncwarp();
-  __nv_bfloat16* o = p.out + ((int64_t)row * p.H + h) * D + lane * VPL;
+  __nv_bfloat16* o =
+      p.out + ((int64_t)row * p.H + h) * D + part * (D / kParts) + lane * VPL;
   float acc[VPL];
 #pragma unroll
   for (int e = 0; e < VPL; ++e) acc[e] = 0.f;
@@ -327,7 +329,7 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
       static_assert(K >= 1 && (K & (K - 1)) == 0, "rotated halves must span whole lanes");
       if (!kLdg) angle = row_angle<R>(p, row, lane);
       const float sn = angle.x, cs = angle.y;
-      const bool rot = lane >= L0;
+      const bool rot = part == kParts - 1 && lane >= L0;
       const bool first = rot && lane - L0 < K;
       const int jb = rot ? ((lane - L0) % K) * VPL : 0;
 #pragma unroll
@@ -342,33 +344,41 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
   uint32_t packed[NW];
 #pragma unroll
   for (int i = 0; i < NW; ++i) packed[i] = pack_bf16(acc[2 * i], acc[2 * i + 1]);
-  if constexpr (VPL == 16) {
-    reinterpret_cast<uint4*>(o)[0] = *reinterpret_cast<const uint4*>(&packed[0]);
-    reinterpret_cast<uint4*>(o)[1] = *reinterpret_cast<const uint4*>(&packed[4]);
-  } else {
+  if constexpr (VPL == 8)
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(&packed[0]);
+  else
     *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(&packed[0]);
-  }
-  if (p.lse && lane == 0)
+  if (p.lse && lane == 0 && part == 0)
     p.lse[(int64_t)row * p.H + h] =
         zero ? (z == INFINITY ? INFINITY : -INFINITY) : (M + log2f(L)) / LOG2E;
 }
 
 // The split merge as its own kernel (several splits per row when the
-// in-cluster merge is not available): one warp per (row, head), four per CTA.
+// in-cluster merge is not available): kMergeParts warps per (row, head), four
+// per CTA.  Rows times heads are few, so it is the latency of a warp's work
+// that counts: at D = 512 the whole call of 8 rows, 128 heads and 9 splits takes
+// 18.9 us with four warps a head, 19.4 with two, 20.9 with one (four rows, 18
+// splits: 18.5, 18.6, 20.8).
+template <int D>
+constexpr int kMergeParts = D / 128;
 template <int D, int R, int G>
 __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int rows) {
+  constexpr int kParts = kMergeParts<D>;
   extern __shared__ float wsm[];  // [4 warps][S] split weights
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t gw = (int64_t)blockIdx.x * 4 + warp;
-  const bool live = gw < (int64_t)rows * p.H;
-  const int row = live ? (int)(gw / p.H) : 0, h = live ? (int)(gw % p.H) : 0;
+  const int part = (int)(gw % kParts);
+  const int64_t gh = gw / kParts;
+  const bool live = gh < (int64_t)rows * p.H;
+  const int row = live ? (int)(gh / p.H) : 0, h = live ? (int)(gh % p.H) : 0;
   // Caller inputs, read and turned into angles while the attention still runs.
   const float z = p.sink[h];
-  const float2 angle = row_angle<R>(p, row, lane);
+  float2 angle = make_float2(0.f, 1.f);
+  if (part == kParts - 1) angle = row_angle<R>(p, row, lane);
   pdl_wait();  // the partials come from the attention kernel
   if (!live) return;
-  merge_head<D, R, G, true>(p, z, angle, row, h, lane, wsm + warp * p.splits);
+  merge_head<D, R, G, kParts, true>(p, z, angle, row, h, part, lane, wsm + warp * p.splits);
 }
 
 template <int D, int R, bool kMx>
@@ -1364,7 +1374,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kAlloc);
   }
-  if (kClusterMerge<D> && p.cluster_merge) {
+  if constexpr (kClusterMerge<D>) if (p.cluster_merge) {
     // Every CTA of the cluster (the S splits of this head group) has written
     // its partial and its (max, sum): the release / acquire cluster barrier
     // publishes them, and CTA `split` then merges heads split, split + S, ...
@@ -1376,7 +1386,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     const int nh = pair ? min(HC, p.H - hg0) : p.H;
     float* wsplit = reinterpret_cast<float*>(stages) + warp * 32;  // S <= 16 weights
     for (int j = split + p.splits * warp; j < nh; j += p.splits * NW)
-      merge_head<D, R, 4, false>(p, 0.f, make_float2(0.f, 1.f), row, hg0 + j, lane, wsplit);
+      merge_head<D, R, 4, 1, false>(p, 0.f, make_float2(0.f, 1.f), row, hg0 + j, 0, lane, wsplit);
   }
 }
 
@@ -1495,7 +1505,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (p.fused) return cudaSuccess;  // the attention kernel finished the rows
   if (a.emit_partials) return cudaSuccess;  // the caller merges the partials
-  const unsigned nblk = (unsigned)(((int64_t)rows * a.H + 3) / 4);
+  const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
   // Groups of 8 or 16 splits (the first group's loads go out with the
   // (max, sum) pairs).
@@ -1520,7 +1530,7 @@ cudaError_t launch_merge_impl(const MqaLaunch& a, cudaStream_t stream) {
   p.lse = a.lse;
   for (int j = 0; j < 64; ++j) p.inv_freq[j] = a.inv_freq[j];
   const int rows = a.B * a.Q;
-  const unsigned nblk = (unsigned)(((int64_t)rows * a.H + 3) / 4);
+  const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
   auto merge = a.splits <= 8 ? mqa_combine_kernel<D, R, 8> : mqa_combine_kernel<D, R, 16>;
   return launch_pdl(merge, dim3(nblk), dim3(128), wsm, stream, 0, a.chained, p, rows);
