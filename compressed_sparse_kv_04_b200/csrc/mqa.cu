@@ -381,6 +381,20 @@ __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int ro
   merge_head<D, R, G, kParts, true>(p, z, angle, row, h, part, lane, wsm + warp * p.splits);
 }
 
+// The merge kernel for `splits` splits: the smallest group that takes them in
+// one round of loads (they go out with the (max, sum) pairs; a further round
+// costs 1.2 to 1.5 us), up to 40.  Whole calls at D = 512: 18 splits 17.3 us, in
+// groups of 16 18.6; 37 splits 22.3, in groups of 24 23.5; 66 splits 21.5, in
+// groups of 24 23.2.  At D = 128, few warps with cold code, groups of 40 lose
+// (66 splits 15.2 us, 14.5 in groups of 24).
+template <int D, int R>
+auto merge_kernel(int splits) {
+  if (splits <= 8) return mqa_combine_kernel<D, R, 8>;
+  if (splits <= 16) return mqa_combine_kernel<D, R, 16>;
+  if (splits <= 24 || D == 128) return mqa_combine_kernel<D, R, 24>;
+  return mqa_combine_kernel<D, R, D == 128 ? 24 : 40>;
+}
+
 template <int D, int R, bool kMx>
 __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     mqa_heads_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -1507,10 +1521,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   if (a.emit_partials) return cudaSuccess;  // the caller merges the partials
   const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
-  // Groups of 8 or 16 splits (the first group's loads go out with the
-  // (max, sum) pairs).
-  auto merge = a.splits <= 8 ? mqa_combine_kernel<D, R, 8> : mqa_combine_kernel<D, R, 16>;
-  return launch_pdl(merge, dim3(nblk), dim3(128), wsm, stream, 0, 1, p, rows);
+  return launch_pdl(merge_kernel<D, R>(a.splits), dim3(nblk), dim3(128), wsm, stream, 0, 1, p, rows);
 }
 
 template <int D, int R>
@@ -1532,8 +1543,7 @@ cudaError_t launch_merge_impl(const MqaLaunch& a, cudaStream_t stream) {
   const int rows = a.B * a.Q;
   const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
-  auto merge = a.splits <= 8 ? mqa_combine_kernel<D, R, 8> : mqa_combine_kernel<D, R, 16>;
-  return launch_pdl(merge, dim3(nblk), dim3(128), wsm, stream, 0, a.chained, p, rows);
+  return launch_pdl(merge_kernel<D, R>(a.splits), dim3(nblk), dim3(128), wsm, stream, 0, a.chained, p, rows);
 }
 
 }  // namespace
