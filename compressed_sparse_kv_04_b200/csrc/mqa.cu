@@ -130,6 +130,7 @@ struct Params {
   int64_t pos_base;
   const int32_t* sel_idx;
   const int32_t* sel_cnt;
+  int late_sel;  // the selection comes from an earlier kernel of the call
   int kmax;
   const __nv_bfloat16* kv_c;
   const uint8_t* kv4;  // MXFP4 cache rows [B, N_cap, mx_row_bytes(D)] (kMx kernels)
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
   // the call) come first in launch order, so CTAs that start late, on SMs the
   // top-k frees, hold only selected tiles.
   int gx = (int)blockIdx.x, gy = (int)blockIdx.y;
-  if (p.Q == 1 && p.sel_idx != nullptr && !p.cluster_merge && p.splits > 1) {
+  if (p.Q == 1 && p.sel_idx != nullptr && (!kMx || p.late_sel) && !p.cluster_merge &&
+      p.splits > 1) {
     const int64_t G = (int64_t)gridDim.x / p.splits;  // head groups per row
     const int64_t ng = G * gridDim.y;
     const int64_t L = (int64_t)blockIdx.x + (int64_t)gridDim.x * blockIdx.y;
@@ -468,10 +470,27 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
   const int n_list = p.sel_idx ? p.kmax : (int)n_vis;
   const int tiles_c = (n_list + TN - 1) / TN;
   const int tiles_all = tiles_c + (nwin + TN - 1) / TN;
+  // Equal runs of the list: the window tiles, which wait for no other kernel of
+  // the call, in the last split.
   const int tps = (tiles_all + p.splits - 1) / p.splits;
-  const int t0 = std::min(split * tps, tiles_all);
-  const int t1 = std::min(t0 + tps, tiles_all);
-  const int ntile = t1 - t0;
+  int t0 = std::min(split * tps, tiles_all);
+  const int ntile = std::min(tps, tiles_all - t0);
+  // An MXFP4 cache, nothing to wait for, no split shorter than the others: one
+  // window tile each in the last splits, and first in them.  It takes the
+  // transform warps 2.6 us, an entry tile 0.5, and is done when the queries are.
+  // (8 sequences, 1024 selected and two window tiles: 17.8 us; 18.9 with both in
+  // the last split.  Where that one is shorter, 34 tiles in runs of 4: 20.9
+  // spread, 20.6 in the last split.)
+  int win_n = 0, win_0 = 0;  // tile `it` is win_0 + it below win_n, else t0 + it
+  if (kMx && !p.late_sel && tps > 1 && tiles_all == p.splits * tps) {
+    const int wins = tiles_all - tiles_c, w = split - (p.splits - wins);
+    if (wins <= p.splits && w >= 0) {
+      win_n = 1;
+      win_0 = tiles_c + w;
+      t0 -= w + 1;
+    }
+  }
+  auto tile_at = [&](int it) { return kMx && it < win_n ? win_0 + it : t0 + it; };
   auto sel_count = [&]() -> int {
     if (!p.sel_idx) return (int)n_vis;
     const int c = p.sel_cnt[row];
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
   };
   // The selection count is read only by CTAs with selected tiles (after
   // their wait).
-  const bool sel_tiles = p.sel_idx != nullptr && t0 < tiles_c;
+  const bool sel_tiles = p.sel_idx != nullptr && t0 + win_n < tiles_c && win_n < ntile;
 
   float* pml = p.part_ml + ((int64_t)row * p.splits + split) * 2 * p.H;
 
@@ -549,29 +568,30 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
                     c * 64, row * p.H + hg0);
     }
     bool waited = false;
-    auto ensure = [&](int t) {
-      if (!waited && !tile_safe(t)) {
+    auto ensure = [&](int it) {
+      if (!waited && !tile_safe(tile_at(it))) {
         pdl_wait();
         waited = true;
       }
     };
     // Selected indices of the next tile are loaded one tile ahead, and
     // independently of the selection count (both round trips overlap).
-    auto load_idx = [&](int t, int hh) -> int64_t {
-      const int j = t * TN + lane + 32 * hh;
+    auto load_idx = [&](int it, int hh) -> int64_t {
+      const int t = tile_at(it), j = t * TN + lane + 32 * hh;
       return (p.sel_idx && t < tiles_c && j < p.kmax) ? (int64_t)p.sel_idx[(int64_t)row * p.kmax + j]
                                                        : 0;
     };
-    if (t0 < t1) ensure(t0);
-    int64_t nxt0 = t0 < t1 ? load_idx(t0, 0) : 0, nxt1 = t0 < t1 ? load_idx(t0, 1) : 0;
+    if (ntile > 0) ensure(0);
+    int64_t nxt0 = ntile > 0 ? load_idx(0, 0) : 0, nxt1 = ntile > 0 ? load_idx(0, 1) : 0;
     const int n_c = sel_tiles ? sel_count() : (p.sel_idx ? 0 : (int)n_vis);
     int it = 0;
-    for (int t = t0; t < t1; ++t, ++it) {
+    for (; it < ntile; ++it) {
+      const int t = tile_at(it);
       const int64_t cur[2] = {nxt0, nxt1};
-      if (t + 1 < t1) {
-        ensure(t + 1);
-        nxt0 = load_idx(t + 1, 0);
-        nxt1 = load_idx(t + 1, 1);
+      if (it + 1 < ntile) {
+        ensure(it + 1);
+        nxt0 = load_idx(it + 1, 0);
+        nxt1 = load_idx(it + 1, 1);
       }
       const int s = it % C::kStages;
       const uint32_t ph = (it / C::kStages) & 1;
@@ -641,7 +661,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     }
     if (*abort_flag && lane == 0) {  // box copies still in flight must land first
       for (int j = std::max(0, it - C::kStages); j < it; ++j)
-        if (t0 + j >= tiles_c || (!kMx && p.sel_idx == nullptr))
+        if (tile_at(j) >= tiles_c || (!kMx && p.sel_idx == nullptr))
           mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, p.status);
     }
     // A CTA whose tiles were all safe still waits once, so that the grid
@@ -938,7 +958,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
 #pragma unroll 1
       for (int it = -1; it < ntile; ++it) {
         // Fetch tile it + 1.
-        const int t = t0 + it + 1;
+        const int t = tile_at(it + 1);
         if (it + 1 < ntile && t < tiles_c) {
           if (!waited && !tile_safe(t)) {
             pdl_wait();
@@ -967,7 +987,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         if (it >= 0) {
           const int s = it % C::kStages;
           mbar_arrive(&full[s]);
-          if (t0 + it >= tiles_c) {
+          if (tile_at(it) >= tiles_c) {
             if (!transform(it)) break;
           } else {
             if (!wait_all(&full[s], (it / C::kStages) & 1, p, abort_flag)) break;
@@ -1459,6 +1479,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   p.pos_base = a.pos_base;
   p.sel_idx = a.sel_idx;
   p.sel_cnt = a.sel_cnt;
+  p.late_sel = a.chained && a.sel_idx != nullptr;
   p.safe_pos = a.safe_pos;
   p.safe_fixed = a.safe_fixed;
   p.kv_c = reinterpret_cast<const __nv_bfloat16*>(a.kv_c);

@@ -146,6 +146,15 @@ def test_many_splits_and_the_largest_selection(orc):
     Case(80, 512, 64, 64, 128, 4, [900 + i for i in range(80)], 300, k=64).check(orc)  # one split
 
 
+def test_window_tiles_spread_over_full_splits(orc):
+    """Calls whose tiles fill every split alike (on 148 multiprocessors), with
+    one, two and five window tiles, ragged lengths among the rows."""
+    Case(8, 512, 128, 64, 128, 4, [4404 - i for i in range(8)], 1100, k=1024).check(orc)
+    Case(8, 512, 128, 64, 320, 4, [3327 - 40 * i for i in range(8)], 832, gains=True).check(orc)
+    Case(9, 128, 16, 32, 128, 4, [7679 - 500 * i for i in range(9)], 1920).check(orc)
+    Case(148, 512, 3, 64, 64, 4, [255 + i for i in range(148)], 100, k=64).check(orc)  # one split
+
+
 @pytest.mark.parametrize("k", [0, 100])
 def test_large_and_small_scales(orc, k):
     """Entries whose scale bytes exceed 128 (values above 12), and entries well
