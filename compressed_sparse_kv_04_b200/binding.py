@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libcsa.so (include/csa.h), same entry-point names.
+"""Thin binding of libcsa.so (include/csa.h), same entry-point names: ctypes, and
+for the short calls of the 4-bit cache the native module _calls.
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch tensors on the current CUDA device; the current torch
@@ -68,6 +69,26 @@ def lib():
         _declare(L)
         _lib = L
     return _lib
+
+
+_calls = None
+
+
+def _native():
+    """The native calls, on the loaded library's entry points."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise RuntimeError("_calls.so not found or not loadable; build it with "
+                               "`python -m compressed_sparse_kv_04_b200.build`") from e
+        m.bind(*(C.cast(f, C.c_void_p).value for f in (
+            L.mxfp4_row_bytes, L.mxfp4_cache_write, L.mxfp4_cache_read,
+            L.sparse_mqa_decode_mxfp4, L.dense_mqa_decode_mxfp4)))
+        _calls = m
+    return _calls
 
 
 def _declare(L):
@@ -573,37 +594,18 @@ def _empty(dev, stream, *shape):
 def mxfp4_cache_write(p, rows, kv4, first_entry=None, count=None, dev_status=None, stream=None):
     """Quantises rows [B, n, d] (bf16; each sequence's rows contiguous) into
     entries first_entry[b] + i, i < count[b], of kv4."""
-    dev = _device()
-    B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
-    if rows.dtype is not torch.bfloat16 or rows.shape != (B, n, d):
-        raise ValueError(f"rows must be bfloat16 [{B}, n, {d}], not {rows.dtype} "
-                         f"{list(rows.shape)}")
-    seq, row, one = rows.stride()
-    if n and (one != 1 or (n > 1 and row != d)):
-        raise ValueError("each sequence's rows must be contiguous")
-    if rows.get_device() != dev:
-        raise ValueError("rows must be on the current CUDA device")
-    _check(lib().mxfp4_cache_write(
-        C.byref(p), rows.data_ptr(), seq if B > 1 else n * d, n,
-        _need(dev, first_entry, "first_entry", torch.int64, B),
-        _need(dev, count, "count", torch.int64, B),
-        _need(dev, kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N, _status(dev, dev_status),
-        _raw_stream(dev, stream)))
+    st = (_calls or _native()).cache_write(p, rows, kv4, first_entry, count, dev_status, stream)
+    if st:
+        _check(st)
 
 
 def mxfp4_cache_read(p, kv4, rows, idx=None, first_entry=None, count=None, dev_status=None,
                      stream=None):
     """The values of entries idx[b, i] (int32, -1 skipped) or first_entry[b] + i,
     i < count[b], of kv4 into rows [B, n, d] (bf16)."""
-    dev = _device()
-    B, d, n, N = p.B, p.d, _size(rows, "rows", 1), _size(kv4, "kv4", 1)
-    out = _need(dev, rows, "rows", torch.bfloat16, B, n, d)
-    _check(lib().mxfp4_cache_read(
-        C.byref(p), _need(dev, kv4, "kv4", torch.uint8, B, N, _row_bytes(d)), N,
-        _need(dev, idx, "idx", torch.int32, B, n),
-        _need(dev, first_entry, "first_entry", torch.int64, B),
-        _need(dev, count, "count", torch.int64, B), n, out, _status(dev, dev_status),
-        _raw_stream(dev, stream)))
+    st = (_calls or _native()).cache_read(p, kv4, rows, idx, first_entry, count, dev_status, stream)
+    if st:
+        _check(st)
 
 
 def _pool_args(dev, p, w_s, b_pos, gamma):
@@ -663,25 +665,19 @@ def _mqa_inputs(dev, p, rows, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
 def sparse_mqa_decode_mxfp4(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink, out, gamma_q=None,
                             gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
     """sparse_mqa_decode over a 4-bit cache."""
-    dev = _device()
-    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
-    _check(lib().sparse_mqa_decode_mxfp4(
-        C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
-        _need(dev, topk_idx, "topk_idx", torch.int32, p.B, p.k),
-        _need(dev, topk_cnt, "topk_cnt", torch.int32, p.B), a["kv_tok"], kv_tok.shape[1], a["sink"],
-        a["gq"], a["gkv"], a["out"], a["lse"], *_ws(dev, ws), _status(dev, dev_status),
-        _raw_stream(dev, stream)))
+    st = (_calls or _native()).sparse_decode(p, q, pos_q, kv4, topk_idx, topk_cnt, kv_tok, sink,
+                                             out, gamma_q, gamma_kv, lse, ws, dev_status, stream)
+    if st:
+        _check(st)
 
 
 def dense_mqa_decode_mxfp4(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q=None, gamma_kv=None,
                            lse=None, ws=None, dev_status=None, stream=None):
     """dense_mqa_decode over a 4-bit cache."""
-    dev = _device()
-    a = _mqa_inputs(dev, p, p.B, q, kv4, kv_tok, sink, out, gamma_q, gamma_kv, lse)
-    _check(lib().dense_mqa_decode_mxfp4(
-        C.byref(p), a["q"], _need(dev, pos_q, "pos_q", torch.int64, p.B), a["kv4"], kv4.shape[1],
-        a["kv_tok"], kv_tok.shape[1], a["sink"], a["gq"], a["gkv"], a["out"], a["lse"], *_ws(dev, ws),
-        _status(dev, dev_status), _raw_stream(dev, stream)))
+    st = (_calls or _native()).dense_decode(p, q, pos_q, kv4, kv_tok, sink, out, gamma_q, gamma_kv,
+                                            lse, ws, dev_status, stream)
+    if st:
+        _check(st)
 
 
 def csa_prefill_chunk_mxfp4(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv4,

@@ -1,4 +1,5 @@
-"""Build libcsa.so in-tree for sm_100a (nvcc, one object per .cu, then link).
+"""Build libcsa.so in-tree for sm_100a (nvcc, one object per .cu, then link)
+and _calls.so, the binding's native calls (g++, against torch's headers).
 
     python -m compressed_sparse_kv_04_b200.build [--force]
 """
@@ -8,12 +9,15 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcsa.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 HEADER = os.path.join(ROOT, "include", "csa.h")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -40,10 +44,27 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _compile_calls() -> None:
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), CALLS_SRC,
+           "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -53,7 +74,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        calls = ex.submit(_compile_calls)
         results = list(ex.map(_compile, srcs))
+        calls.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

@@ -178,3 +178,28 @@ def test_workspace_is_checked_like_every_tensor():
     with pytest.raises(TypeError, match="ws"):
         binding._ws(binding._device(), 16)
     assert binding._ws(binding._device(), None) == (None, 0)
+
+
+def test_native_calls_check_every_argument():
+    """Wrong types, shapes and places, each named; the library is not reached."""
+    p = P(B=2, d=128, H=4, rope_dim=32, k=8)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    q, kv4, tok = bf(2, 4, 128), torch.zeros(2, 8, 80, dtype=torch.uint8), bf(2, 9, 128)
+    pos, sink, out = torch.zeros(2, dtype=torch.int64), torch.zeros(4), bf(2, 4, 128)
+    idx, cnt = torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    dense = dict(p=p, q=q, pos_q=pos, kv4=kv4, kv_tok=tok, sink=sink, out=out)
+    sparse = dict(dense, topk_idx=idx, topk_cnt=cnt)
+    bad = [("q", bf(2, 4, 64), ValueError), ("q", 3, TypeError), ("kv4", None, TypeError),
+           ("kv4", torch.zeros(2), ValueError), ("kv_tok", None, TypeError),
+           ("q", torch.zeros(2, 4, 128), ValueError), ("p", kv4, TypeError)]
+    for fn, args in ((binding.dense_mqa_decode_mxfp4, dense),
+                     (binding.sparse_mqa_decode_mxfp4, sparse)):
+        for name, value, error in bad:
+            with pytest.raises(error, match=None if name == "p" else name):
+                fn(**dict(args, **{name: value}))
+        with pytest.raises(ValueError, match="q is on cpu"):
+            fn(**args)
+    with pytest.raises(binding.CsaError):
+        binding.mxfp4_cache_read(P(d=256), kv4, bf(2, 3, 256))
+    with pytest.raises(TypeError):
+        binding._native().cache_write(p)
