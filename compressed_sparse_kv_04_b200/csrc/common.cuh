@@ -331,6 +331,12 @@ CSA_DEV void tmem_st_16x32bx2_x32(uint32_t taddr, const uint32_t (&r)[32]) {
 // pdl_trigger() lets the next kernel in the stream be scheduled early.
 CSA_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 CSA_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Every thread of a call's first kernel in head mode (see launch_pdl), before it
+// reads anything of the caller's.
+CSA_DEV void pdl_head() {
+  pdl_wait();
+  pdl_trigger();
+}
 
 CSA_DEV void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -251,11 +251,12 @@ int device_sm_count();
 // chained == 0 (the first kernel of an entry point): an ordinary launch,
 // which starts after all earlier work in the stream has completed, whatever
 // that work is (a caller's kernel that lets its dependents start early
-// included).  The decode steps' first kernel (compression) instead runs in
-// a head mode: launched with programmatic serialization, it waits for the
-// previous kernel before it reads anything and triggers its dependents only
-// after that wait, which gives the same guarantee while its launch overlaps
-// the previous kernel.
+// included).  The decode steps' first kernel (compression), and those of the
+// calls on 4-bit data (cache write and read, the attention on its own, the
+// quantiser), instead run in a head mode: launched with programmatic
+// serialization, they wait for the previous kernel before they read anything
+// and trigger their dependents only after that wait, which gives the same
+// guarantee while the launch overlaps the previous kernel.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, int cluster_x, int chained, Args... args) {

@@ -131,6 +131,7 @@ struct Params {
   const int32_t* sel_idx;
   const int32_t* sel_cnt;
   int late_sel;  // the selection comes from an earlier kernel of the call
+  int pdl_head;  // this is the call's first kernel, in head mode (see launch_pdl)
   int kmax;
   const __nv_bfloat16* kv_c;
   const uint8_t* kv4;  // MXFP4 cache rows [B, N_cap, mx_row_bytes(D)] (kMx kernels)
@@ -430,7 +431,34 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       (reinterpret_cast<uintptr_t>(abort_flag + 1) + 15) & ~uintptr_t(15));
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1 + NT);  // producer + the transform threads
+      mbar_init(&ready[s], NT);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sfull[a], 1);
+      mbar_init(&pfull[a], 128);
+    }
+    mbar_init(&pvdone[0], 1);
+    mbar_init(&pvdone[1], 1);
+    mbar_init(qready, 128);
+    mbar_init(drain, 1);
+    mbar_init(done, NW);
+    mbar_init(qfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, C::kAlloc);
+    tmem_relinquish();
+  }
+  if (kMx && p.pdl_head)
+    pdl_head();
+  else
+    pdl_trigger();
   // H > 64: CTA g*S + s (g = 0, 1) owns heads [64g, 64g+64) of split s, so
   // the S splits of one head group are consecutive (one cluster when the
   // partials are merged in-cluster).
@@ -522,30 +550,6 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
 
   float* pml = p.part_ml + ((int64_t)row * p.splits + split) * 2 * p.H;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + NT);  // producer + the transform threads
-      mbar_init(&ready[s], NT);
-      mbar_init(&empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&sfull[a], 1);
-      mbar_init(&pfull[a], 128);
-    }
-    mbar_init(&pvdone[0], 1);
-    mbar_init(&pvdone[1], 1);
-    mbar_init(qready, 128);
-    mbar_init(drain, 1);
-    mbar_init(done, NW);
-    mbar_init(qfull, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncwarp();
-  if (warp == 0) {
-    tmem_alloc(tmem_slot, C::kAlloc);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1480,6 +1484,8 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   p.sel_idx = a.sel_idx;
   p.sel_cnt = a.sel_cnt;
   p.late_sel = a.chained && a.sel_idx != nullptr;
+  p.pdl_head = kMx && !a.chained;
+  const int pdl = a.chained || p.pdl_head;
   p.safe_pos = a.safe_pos;
   p.safe_fixed = a.safe_fixed;
   p.kv_c = reinterpret_cast<const __nv_bfloat16*>(a.kv_c);
@@ -1532,11 +1538,11 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
           clusters_resident(reinterpret_cast<const void*>(kern), variant, kBlockThreads<kMx>,
                             a.splits, smem)) {
     p.cluster_merge = 1;
-    return launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, a.splits, a.chained, map_q,
+    return launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, a.splits, pdl, map_q,
                       box_c, box_t, p);
   }
-  e = launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, 0, a.chained, map_q, box_c,
-                 box_t, p);
+  e = launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, 0, pdl, map_q, box_c, box_t,
+                 p);
   if (e != cudaSuccess) return e;
   if (p.fused) return cudaSuccess;  // the attention kernel finished the rows
   if (a.emit_partials) return cudaSuccess;  // the caller merges the partials

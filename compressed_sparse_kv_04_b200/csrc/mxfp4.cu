@@ -107,6 +107,7 @@ CSA_DEV void write_rows(const WriteArgs& a, const Range& rg) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a) {
+  pdl_head();
   const Range rg(a.first, a.count, blockIdx.y, a.n);
   if (rg.whole((int64_t)blockIdx.x * Rows<D>::kRows, Rows<D>::kRows, a.n_cap))
     write_rows<D, true>(a, rg);
@@ -184,6 +185,7 @@ CSA_DEV void read_rows(const ReadArgs& a, const Range& rg) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) {
+  pdl_head();
   const Range rg(a.first, a.count, blockIdx.y, a.n);
   if (!a.idx && rg.whole((int64_t)blockIdx.x * Rows<D>::kRows, Rows<D>::kRows, a.n_cap))
     read_rows<D, true>(a, rg);
@@ -201,8 +203,8 @@ cudaError_t launch_mx_cache_write(const MxCacheLaunch& c, cudaStream_t stream) {
   if (gx == 0) return cudaSuccess;
   if (gx > 0x7FFFFFFF || c.B > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)gx, (unsigned)c.B);
-  if (c.d == 512) return launch_pdl(cache_write_kernel<512>, grid, dim3(kThreads), 0, stream, 0, 0, a);
-  if (c.d == 128) return launch_pdl(cache_write_kernel<128>, grid, dim3(kThreads), 0, stream, 0, 0, a);
+  if (c.d == 512) return launch_pdl(cache_write_kernel<512>, grid, dim3(kThreads), 0, stream, 0, 1, a);
+  if (c.d == 128) return launch_pdl(cache_write_kernel<128>, grid, dim3(kThreads), 0, stream, 0, 1, a);
   return cudaErrorInvalidValue;
 }
 
@@ -214,8 +216,8 @@ cudaError_t launch_mx_cache_read(const MxCacheLaunch& c, cudaStream_t stream) {
   if (gx == 0) return cudaSuccess;
   if (gx > 0x7FFFFFFF || c.B > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)gx, (unsigned)c.B);
-  if (c.d == 512) return launch_pdl(cache_read_kernel<512>, grid, dim3(kThreads), 0, stream, 0, 0, a);
-  if (c.d == 128) return launch_pdl(cache_read_kernel<128>, grid, dim3(kThreads), 0, stream, 0, 0, a);
+  if (c.d == 512) return launch_pdl(cache_read_kernel<512>, grid, dim3(kThreads), 0, stream, 0, 1, a);
+  if (c.d == 128) return launch_pdl(cache_read_kernel<128>, grid, dim3(kThreads), 0, stream, 0, 1, a);
   return cudaErrorInvalidValue;
 }
 

@@ -688,13 +688,13 @@ __global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* __restr
                                                           int64_t cols, uint8_t* codes,
                                                           uint8_t* scales) {
   constexpr int kU = 8;  // rows in flight per warp
+  pdl_head();
   __shared__ __align__(16) uint8_t sc[2][kScaleTile];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 256;
   const bool in = k0 + 8 * lane < cols;
   const uint8_t* src = x + (r0 + warp) * ld_bytes + (k0 + 8 * lane) * 2;
   uint8_t* dst = codes + (r0 + warp) * (cols / 2) + (k0 + 8 * lane) / 2;
-  pdl_trigger();
   const int live = (int)min((int64_t)128, rows - r0);
   if (threadIdx.x < 2 * kScaleTile / 16)  // rows past the last one: zeros
     reinterpret_cast<uint4*>(&sc[0][0])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
@@ -852,7 +852,7 @@ cudaError_t launch_pair(const MxGemm& g, cudaStream_t stream) {
 cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t cols, void* codes,
                                void* scales, cudaStream_t stream) {
   const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((rows + 127) / 128));
-  return launch_pdl(mx_quantise_kernel, grid, dim3(256), 0, stream, 0, 0,
+  return launch_pdl(mx_quantise_kernel, grid, dim3(256), 0, stream, 0, 1,
                     static_cast<const uint8_t*>(x), ld * 2, rows, cols,
                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }

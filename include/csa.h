@@ -29,8 +29,9 @@
  *   - Ordering: the first kernel of every call starts its work only after
  *     all earlier work on the stream has completed -- including a caller's
  *     kernel that lets its dependents launch early.  (It is an ordinary
- *     launch, except in the decode steps, where it may be scheduled early
- *     but waits for the previous kernel before reading anything.)
+ *     launch, except in the decode steps and in the MXFP4 calls, where it may
+ *     be scheduled early but waits for the previous kernel before reading
+ *     anything.)
  *     The later kernels of a call may start while their predecessor in the
  *     same call still runs (programmatic dependent launch) and read the
  *     call's inputs early; they wait for that predecessor before reading

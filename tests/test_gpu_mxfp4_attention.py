@@ -353,6 +353,51 @@ def test_two_streams_two_workspaces():
     assert torch.equal(oa, ra) and torch.equal(ob, rb)
 
 
+@pytest.mark.parametrize("k", [0, 128])
+def test_back_to_back_calls_behind_other_work(k):
+    """Calls that follow copies and one another (each may be scheduled while the
+    one before still runs), eager and captured: the same outputs every time."""
+    c = Case(8, 512, 128, 64, 128, 4, [4000 - 100 * i for i in range(8)], 1024, k=k, seed=9)
+    op = binding.OP_SPARSE_MQA if k else binding.OP_DENSE_MQA
+    ws = binding.workspace(c.p, op, 1, 1024)
+    qs = [c.q, -c.q, c.q.roll(1, 0)]
+    want = []
+    for q in qs:
+        c.q = q
+        want.append(c.run(c.kv4)[0])
+    q, cache = torch.empty_like(qs[0]), torch.empty_like(c.kv4)
+    outs = [torch.empty_like(w) for w in want]
+
+    def chain():
+        cache.copy_(c.kv4)
+        for x, out in zip(qs, outs):
+            q.copy_(x)
+            if k:
+                binding.sparse_mqa_decode_mxfp4(c.p, q, c.pos, cache, c.sel, c.cnt, c.kv_tok,
+                                                c.sink, out, ws=ws)
+            else:
+                binding.dense_mqa_decode_mxfp4(c.p, q, c.pos, cache, c.kv_tok, c.sink, out, ws=ws)
+        cache.zero_()
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        for o in outs:
+            o.zero_()
+
+    for _ in range(10):
+        chain()
+        check()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        chain()
+    for _ in range(10):
+        g.replay()
+        check()
+
+
 def _step_inputs(w, L_cap):
     kv_tok, idx_tok = synth.token_streams(w, L_cap=L_cap, device=DEV)
     return kv_tok, idx_tok, synth.pool_params(w, DEV), (

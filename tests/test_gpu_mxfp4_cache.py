@@ -199,3 +199,59 @@ def test_compression_into_the_cache(name, kw):
         n = min(first + nb, -(-int(ctx[b]) // m))  # blocks with a token
         assert np.array_equal(got[b, first:n], mxref.cache_rows(bits[b, first:n], 0xAB)), b
         assert (got[b, :first] == 0xAB).all() and (got[b, n:] == 0xAB).all()
+
+
+def _captured(fn):
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        fn(s)
+    return g
+
+
+def test_calls_behind_copies_memsets_and_joined_streams():
+    """The calls' first kernels may be scheduled early: behind a memset, a copy, a
+    kernel and a joined stream, eager and captured, they see what came before."""
+    d, B, n, N = 512, 4, 300, 400
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    p = binding.make_params(B, d)
+    src = torch.randn(B, n, d, generator=gen, device=DEV).bfloat16()
+    rows, back = torch.zeros_like(src), torch.zeros_like(src)
+    kv4, copy = binding.mxfp4_cache(p, N), binding.mxfp4_cache(p, N)
+    binding.mxfp4_cache_write(p, src, kv4)
+    want = torch.empty_like(src)
+    binding.mxfp4_cache_read(p, kv4, want)
+    want4 = kv4.clone()
+    side = torch.cuda.Stream()
+
+    def chain(s):
+        kv4.zero_()
+        rows.copy_(src)
+        binding.mxfp4_cache_write(p, rows, kv4)   # behind a copy
+        copy.copy_(kv4)
+        back.zero_()
+        binding.mxfp4_cache_read(p, copy, back)   # behind a memset
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            rows.neg_()
+            kv4.zero_()
+        s.wait_stream(side)
+        binding.mxfp4_cache_write(p, rows, kv4)   # behind a joined stream
+        binding.mxfp4_cache_read(p, kv4, rows)    # behind a call
+
+    def check():
+        torch.cuda.synchronize()
+        assert torch.equal(back, want)
+        assert torch.equal(rows, -want)
+        assert torch.equal(copy, want4)
+        for t in (kv4, copy, back, rows):
+            t.fill_(1)
+
+    for _ in range(20):
+        chain(torch.cuda.current_stream())
+        check()
+    g = _captured(chain)
+    for _ in range(20):
+        g.replay()
+        check()
