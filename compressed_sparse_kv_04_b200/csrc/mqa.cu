@@ -36,12 +36,9 @@
 //     write P (bf16) to shared memory in the MMA's K-major layout.
 // Splits of the KV list run on different CTAs; their (m, l, O) partials are
 // merged, with the sink folded in and the inverse RoPE applied, by
-// mqa_combine_kernel, or at D = 128 by the CTAs themselves when the S splits
-// of a head group form one thread-block cluster and all clusters of the
-// launch fit at once (S <= 16: a cluster barrier, then each CTA merges a share
-// of the heads from L2).  With one split per row the
-// attention CTA finishes its rows directly.  Every wait is bounded and
-// reports CSA_ERR_DEVICE_TIMEOUT.
+// mqa_combine_kernel, which sets itself up while the attention still runs.
+// With one split per row the attention CTA finishes its rows directly.  Every
+// wait is bounded and reports CSA_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
 
 #include "common.cuh"
@@ -100,14 +97,6 @@ struct MCfg {
   static constexpr uint32_t kAlloc = (D <= 256 && kQCol + D / 2 <= 256) ? 256 : 512;
 };
 
-// Whether a kernel can merge a row's splits inside a cluster.  At D = 512 the
-// merge kernel, which overlaps its start with the attention's end, is faster
-// (4-bit cache, 5 rows of 64 heads: 17.7 us against 20.3; the V4-Flash decode
-// step 42.5 us against 46.4, the 1M one 71.8 against 73.0); at D = 128 the
-// cluster is (10.2 us against 10.8).
-template <int D>
-constexpr bool kClusterMerge = D == 128;
-
 struct Meta {
   int32_t grow[TN];   // row coordinate in the tensor map
   int32_t pos[TN];    // RoPE position
@@ -145,11 +134,6 @@ struct Params {
   // normalisation, inverse rotation, bf16 output and log-sum-exp) and no
   // merge runs.
   int fused;
-  // Several splits per row, launched as one cluster per (row, head group):
-  // after every CTA of the cluster has written its partial, the CTAs merge
-  // them themselves (each a share of the group's heads) and no merge kernel
-  // runs.
-  int cluster_merge;
   const float* sink;
   __nv_bfloat16* out;
   float* lse;
@@ -206,10 +190,8 @@ CSA_DEV bool wait_all(uint64_t* bar, uint32_t parity, const Params& p, volatile 
 
 // Where a merge finds the split partials of one (row, head): lane l's dims
 // (fp16) and the (max, sum) pair of each split.
-// kLdg: they come from an earlier kernel (read-only path); otherwise they were
-// written during this kernel by other CTAs and are read from L2.
 // kParts: warps that share the head's dims (part `part` of them: D / kParts).
-template <int D, int kParts, bool kLdg>
+template <int D, int kParts>
 struct Partials {
   const __half* src;  // split 0's dims of this lane
   const float* ml;    // split 0's maximum of this head
@@ -221,7 +203,7 @@ struct Partials {
         ml(p.part_ml + (int64_t)row * p.splits * 2 * p.H + h), stride((int64_t)p.H * D), H(p.H) {}
   template <typename T>
   CSA_DEV static T ld(const T* a) {
-    return kLdg ? __ldg(a) : __ldcg(a);
+    return __ldg(a);
   }
   CSA_DEV float maximum(int s) const { return ld(ml + (int64_t)s * 2 * H); }
   CSA_DEV float sum(int s) const { return ld(ml + (int64_t)s * 2 * H + H); }
@@ -251,10 +233,10 @@ CSA_DEV float2 row_angle(const Params& p, int row, int lane) {
   return make_float2(sn, cs);
 }
 
-template <int D, int R, int G, int kParts, bool kLdg>
+template <int D, int R, int G, int kParts>
 CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, int part, int lane,
                         float* wsplit) {
-  const Partials<D, kParts, kLdg> src(p, row, h, part, lane);
+  const Partials<D, kParts> src(p, row, h, part, lane);
   constexpr int VPL = D / kParts / 32;  // dims per lane: 8 or 4
   constexpr int NW = VPL / 2;           // 32-bit words (fp16 pairs) per lane and split
   static_assert(VPL == 8 || VPL == 4, "a lane's dims are one load");
@@ -277,7 +259,6 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
     l0 = src.sum(lane);
   }
   const float LOG2E = 1.4426950408889634f;
-  if (!kLdg) z = p.sink[h];  // (the merge kernel read it before its wait)
   const float z2 = z * LOG2E;  // log2 domain
   float M = fmaxf(z2, m0);
   for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, src.maximum(s));
@@ -329,7 +310,6 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
       constexpr int K = R / 2 / VPL;  // lanes per rotated half
       constexpr int L0 = 32 - 2 * K;  // first lane holding rotated dims
       static_assert(K >= 1 && (K & (K - 1)) == 0, "rotated halves must span whole lanes");
-      if (!kLdg) angle = row_angle<R>(p, row, lane);
       const float sn = angle.x, cs = angle.y;
       const bool rot = part == kParts - 1 && lane >= L0;
       const bool first = rot && lane - L0 < K;
@@ -355,12 +335,14 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
         zero ? (z == INFINITY ? INFINITY : -INFINITY) : (M + log2f(L)) / LOG2E;
 }
 
-// The split merge as its own kernel (several splits per row when the
-// in-cluster merge is not available): kMergeParts warps per (row, head), four
-// per CTA.  Rows times heads are few, so it is the latency of a warp's work
-// that counts: at D = 512 the whole call of 8 rows, 128 heads and 9 splits takes
-// 18.9 us with four warps a head, 19.4 with two, 20.9 with one (four rows, 18
-// splits: 18.5, 18.6, 20.8).
+// The split merge: kMergeParts warps per (row, head), four per CTA.  Rows times
+// heads are few, so it is the latency of a warp's work that counts: at D = 512
+// the whole call of 8 rows, 128 heads and 9 splits takes 18.9 us with four warps
+// a head, 19.4 with two, 20.9 with one (four rows, 18 splits: 18.5, 18.6, 20.8).
+// Merged by the attention CTAs themselves instead, the S splits of a head group
+// as one cluster, a call takes 0.6 us more at D = 128 and 6 more at D = 512 (5
+// rows of 64 heads 20.5, 14.5 so): a cluster barrier, then cold code, while this
+// kernel has set itself up before the attention ends.
 template <int D>
 constexpr int kMergeParts = D / 128;
 template <int D, int R, int G>
@@ -380,7 +362,7 @@ __global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int ro
   if (part == kParts - 1) angle = row_angle<R>(p, row, lane);
   pdl_wait();  // the partials come from the attention kernel
   if (!live) return;
-  merge_head<D, R, G, kParts, true>(p, z, angle, row, h, part, lane, wsm + warp * p.splits);
+  merge_head<D, R, G, kParts>(p, z, angle, row, h, part, lane, wsm + warp * p.splits);
 }
 
 // The merge kernel for `splits` splits: the smallest group that takes them in
@@ -459,17 +441,13 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     pdl_head();
   else
     pdl_trigger();
-  // H > 64: CTA g*S + s (g = 0, 1) owns heads [64g, 64g+64) of split s, so
-  // the S splits of one head group are consecutive (one cluster when the
-  // partials are merged in-cluster).
+  // H > 64: CTA g*S + s (g = 0, 1) owns heads [64g, 64g+64) of split s.
   const bool pair = p.H > HC;
-  // Sparse decode without the in-cluster merge: the CTAs of every head
-  // group's last split (the window tiles, which wait for no other kernel of
-  // the call) come first in launch order, so CTAs that start late, on SMs the
-  // top-k frees, hold only selected tiles.
+  // Sparse decode: the CTAs of every head group's last split (the window tiles,
+  // which wait for no other kernel of the call) come first in launch order, so
+  // CTAs that start late, on SMs the top-k frees, hold only selected tiles.
   int gx = (int)blockIdx.x, gy = (int)blockIdx.y;
-  if (p.Q == 1 && p.sel_idx != nullptr && (!kMx || p.late_sel) && !p.cluster_merge &&
-      p.splits > 1) {
+  if (p.Q == 1 && p.sel_idx != nullptr && (!kMx || p.late_sel) && p.splits > 1) {
     const int64_t G = (int64_t)gridDim.x / p.splits;  // head groups per row
     const int64_t ng = G * gridDim.y;
     const int64_t L = (int64_t)blockIdx.x + (int64_t)gridDim.x * blockIdx.y;
@@ -1412,57 +1390,6 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kAlloc);
   }
-  if constexpr (kClusterMerge<D>) if (p.cluster_merge) {
-    // Every CTA of the cluster (the S splits of this head group) has written
-    // its partial and its (max, sum): the release / acquire cluster barrier
-    // publishes them, and CTA `split` then merges heads split, split + S, ...
-    // of the group, one warp per head.  Every thread of every CTA reaches
-    // this point exactly once (no role returns early).
-    __threadfence();
-    __syncwarp();
-    cluster_sync();
-    const int nh = pair ? min(HC, p.H - hg0) : p.H;
-    float* wsplit = reinterpret_cast<float*>(stages) + warp * 32;  // S <= 16 weights
-    for (int j = split + p.splits * warp; j < nh; j += p.splits * NW)
-      merge_head<D, R, 4, 1, false>(p, 0.f, make_float2(0.f, 1.f), row, hg0 + j, 0, lane, wsplit);
-  }
-}
-
-// How many clusters of S attention CTAs (one per SM) can be resident at once
-// on this device (S <= 8 portable, up to 16 with the non-portable cluster
-// size); 0 when none can.  Cached per (device, kernel variant, S).
-int clusters_resident(const void* kern, int variant, int threads, int S, size_t smem) {
-  static int cached[64][16][17] = {};  // 0 unknown, else count + 1
-  if (S < 2 || S > 16) return 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || variant < 0 || variant >= 16)
-    return 0;
-  int& c = cached[dev][variant][S];
-  if (c) return c - 1;
-  bool ok = true;
-  if (S > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                   cudaSuccess)
-    ok = false;
-  if (ok) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(S, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    ok = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n >= 1;
-    c = ok ? n + 1 : 1;
-  } else {
-    c = 1;
-  }
-  if (!ok) cudaGetLastError();  // a refused query is not the caller's error
-  return c - 1;
 }
 
 template <int D, int R, bool kMx>
@@ -1530,17 +1457,6 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   e = ensure_smem_attr(reinterpret_cast<const void*>(kern), (kMx ? 16 : 3) + variant, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(cps * a.splits, rows, 1);
-  // The splits of each head group form one cluster and merge in-kernel, when
-  // every cluster of the launch can be resident at once (otherwise the
-  // clusters would run in waves: the separate merge kernel is faster).
-  if (kClusterMerge<D> && !p.fused && !a.emit_partials &&
-      (int64_t)cps * rows <=
-          clusters_resident(reinterpret_cast<const void*>(kern), variant, kBlockThreads<kMx>,
-                            a.splits, smem)) {
-    p.cluster_merge = 1;
-    return launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, a.splits, pdl, map_q,
-                      box_c, box_t, p);
-  }
   e = launch_pdl(kern, grid, dim3(kBlockThreads<kMx>), smem, stream, 0, pdl, map_q, box_c, box_t,
                  p);
   if (e != cudaSuccess) return e;
