@@ -86,7 +86,7 @@ def _native():
                                "`python -m compressed_sparse_kv_04_b200.build`") from e
         m.bind(*(C.cast(f, C.c_void_p).value for f in (
             L.mxfp4_row_bytes, L.mxfp4_cache_write, L.mxfp4_cache_read,
-            L.sparse_mqa_decode_mxfp4, L.dense_mqa_decode_mxfp4)))
+            L.sparse_mqa_decode_mxfp4, L.dense_mqa_decode_mxfp4, L.grouped_out_proj_mxfp4)))
         _calls = m
     return _calls
 
@@ -793,24 +793,15 @@ def grouped_out_proj_mxfp4(o, w_g, w_g_scale, w_o, w_o_scale, z, y=None, ws=None
     """grouped_out_proj with 4-bit weights and activations: o [T, H, D] bf16,
     w_g [g, d_g, H/g*D/2] and w_o [d_model, g*d_g/2] codes with their scale
     tiles (mxfp4_quantize).  The workspace is allocated here when not given."""
-    dev = _device()
-    if not isinstance(o, torch.Tensor) or o.dim() != 3:
-        raise ValueError("o must be [T, H, D]")
-    T, H, D = o.shape
-    g, d_g = _size(w_g, "w_g", 0), _size(w_g, "w_g", 1)
-    d_model = _size(w_o, "w_o", 0)
+    native = _calls or _native()
     if ws is None:
-        ws = _empty(dev, stream, grouped_out_proj_mxfp4_workspace_bytes(T, H, D, g, d_g, d_model))
-    k1, k2 = H // max(g, 1) * D, g * d_g
-    u8, bf = torch.uint8, torch.bfloat16
-    _check(lib().grouped_out_proj_mxfp4(
-        T, H, D, g, d_g, d_model, _need(dev, o, "o", bf, T, H, D),
-        _need(dev, w_g, "w_g", u8, g, d_g, k1 // 2),
-        _need_scales(dev, w_g_scale, "w_g_scale", -(-k2 // 128) * (k1 // 128) * 512),
-        _need(dev, w_o, "w_o", u8, d_model, k2 // 2),
-        _need_scales(dev, w_o_scale, "w_o_scale", -(-d_model // 128) * (k2 // 128) * 512),
-        _need(dev, y, "y", bf, T, k2), _need(dev, z, "z", bf, T, d_model), *_ws(dev, ws),
-        _status(dev, dev_status), _raw_stream(dev, stream)))
+        if not isinstance(o, torch.Tensor) or o.dim() != 3:
+            raise ValueError("o must be [T, H, D]")
+        ws = _empty(_device(), stream, grouped_out_proj_mxfp4_workspace_bytes(
+            *o.shape, _size(w_g, "w_g", 0), _size(w_g, "w_g", 1), _size(w_o, "w_o", 0)))
+    st = native.out_proj(o, w_g, w_g_scale, w_o, w_o_scale, z, y, ws, dev_status, stream)
+    if st:
+        _check(st)
 
 
 # ------------------------------------------- context split over several devices --

@@ -1,10 +1,11 @@
-// Python calls of the 4-bit cache and its attention: argument checks on torch
-// tensors and the C entry point (include/csa.h) in one step.
+// Python calls of the 4-bit cache, its attention and the 4-bit projection:
+// argument checks on torch tensors and the C entry point (include/csa.h) in one
+// step.
 //
 // These calls are short on the device (a few microseconds), so a program that
 // makes them one by one waits for the host.  Of that a cache write takes 3.2 us
-// here, an attention call 6; through Python checks and ctypes they took 7.4 and
-// 13.  (The launch alone, from C: 2.9.)
+// here, an attention call 6, the projection 8.5; through Python checks and ctypes
+// they took 7.4, 13 and 16.  (One launch alone, from C: 2.9.)
 //
 // The module holds no copy of the library: bind() gets the entry points'
 // addresses from the one that the binding has loaded.
@@ -13,6 +14,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cstdint>
 #include <exception>
 #include <initializer_list>
 #include <sstream>
@@ -27,6 +30,7 @@ decltype(&::mxfp4_cache_write) cache_write = nullptr;
 decltype(&::mxfp4_cache_read) cache_read = nullptr;
 decltype(&::sparse_mqa_decode_mxfp4) sparse_decode = nullptr;
 decltype(&::dense_mqa_decode_mxfp4) dense_decode = nullptr;
+decltype(&::grouped_out_proj_mxfp4) out_proj = nullptr;
 
 // A Python exception is set.
 struct Raised {};
@@ -258,6 +262,55 @@ long do_decode(PyObject* const* a) {
   });
 }
 
+// Scale tiles: `bytes` bytes in any shape.
+const void* need_scales(PyObject* o, const char* name, int dev, int64_t bytes) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != kU8 || t.numel() != bytes) {
+    std::ostringstream s;
+    s << name << " must hold " << bytes << " bytes, not " << t.numel() << " of "
+      << type_name(t.scalar_type());
+    raise(PyExc_ValueError, s.str());
+  }
+  on_device(t, name, dev);
+  if (!t.is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be contiguous");
+  return t.data_ptr();
+}
+
+int checked_int(int64_t v, const char* what) {
+  if (v > INT32_MAX) raise(PyExc_ValueError, std::string(what) + " is too long");
+  return (int)v;
+}
+
+// (o, w_g, w_g_scale, w_o, w_o_scale, z, y, ws, dev_status, stream)
+long do_project(PyObject* const* a) {
+  const int dev = current_device();
+  const at::Tensor& o = tensor(a[0], "o");
+  if (o.dim() != 3) raise(PyExc_ValueError, "o must be [T, H, D]");
+  const int T = checked_int(o.size(0), "o"), H = checked_int(o.size(1), "o"),
+            D = checked_int(o.size(2), "o");
+  const int g = checked_int(length(a[1], "w_g", 0), "w_g"),
+            d_g = checked_int(length(a[1], "w_g", 1), "w_g"),
+            d_model = checked_int(length(a[3], "w_o", 0), "w_o");
+  // (Products of two such sizes fit 64 bits; the library refuses large ones.)
+  const int64_t k1 = (int64_t)(H / std::max(g, 1)) * D, k2 = (int64_t)g * d_g;
+  const void* op = need(a[0], "o", dev, kBf16, {T, H, D});
+  const void* wg = need(a[1], "w_g", dev, kU8, {g, d_g, k1 / 2});
+  const void* wgs = need_scales(a[2], "w_g_scale", dev, (k2 + 127) / 128 * (k1 / 128) * 512);
+  const void* wo = need(a[3], "w_o", dev, kU8, {d_model, k2 / 2});
+  const void* wos =
+      need_scales(a[4], "w_o_scale", dev, ((int64_t)d_model + 127) / 128 * (k2 / 128) * 512);
+  void* z = need(a[5], "z", dev, kBf16, {T, d_model});
+  void* y = need(a[6], "y", dev, kBf16, {T, k2});
+  const auto ws = workspace(a[7], dev);
+  int32_t* status = status_word(a[8], dev);
+  void* stream = raw_stream(a[9], dev);
+  return without_gil([&] {
+    return out_proj(T, H, D, g, d_g, d_model, op, wg, wgs, wo, wos, y, z, ws.first, ws.second,
+                    status, stream);
+  });
+}
+
 // A call of kArgs positional arguments; its csa_status as an int.
 template <long (*kCall)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -274,15 +327,16 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// bind(row_bytes, cache_write, cache_read, sparse_decode, dense_decode): the
-// addresses of the entry points.
+// bind(row_bytes, cache_write, cache_read, sparse_decode, dense_decode, out_proj):
+// the addresses of the entry points.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* f[5];
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+  constexpr int kN = 6;
+  void* f[kN];
+  if (n != kN) {
+    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
     return nullptr;
   }
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < kN; ++i) {
     f[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
     if (!f[i]) {
@@ -295,6 +349,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   cache_read = reinterpret_cast<decltype(cache_read)>(f[2]);
   sparse_decode = reinterpret_cast<decltype(sparse_decode)>(f[3]);
   dense_decode = reinterpret_cast<decltype(dense_decode)>(f[4]);
+  out_proj = reinterpret_cast<decltype(out_proj)>(f[5]);
   Py_RETURN_NONE;
 }
 
@@ -305,10 +360,11 @@ PyMethodDef methods[] = {
     {"cache_read", FAST((entry<do_read, 8>)), "mxfp4_cache_read"},
     {"sparse_decode", FAST((entry<do_decode<true>, 15>)), "sparse_mqa_decode_mxfp4"},
     {"dense_decode", FAST((entry<do_decode<false>, 13>)), "dense_mqa_decode_mxfp4"},
+    {"out_proj", FAST((entry<do_project, 10>)), "grouped_out_proj_mxfp4"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls",
-                      "Checked calls of the 4-bit cache and its attention.", -1, methods,
+                      "Checked calls of the 4-bit cache, its attention and projection.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

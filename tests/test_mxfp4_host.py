@@ -203,3 +203,17 @@ def test_native_calls_check_every_argument():
         binding.mxfp4_cache_read(P(d=256), kv4, bf(2, 3, 256))
     with pytest.raises(TypeError):
         binding._native().cache_write(p)
+
+
+def test_native_projection_checks_every_argument():
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    ok = dict(o=bf(2, 4, 128), w_g=u8(2, 128, 128), w_g_scale=u8(2 * 2 * 512), w_o=u8(256, 128),
+              w_o_scale=u8(2 * 2 * 512), z=bf(2, 256), ws=u8(1 << 16))
+    for name, value, error in (("o", bf(2, 4), ValueError), ("o", None, TypeError),
+                               ("w_g", u8(2, 128), ValueError), ("w_o", None, TypeError),
+                               ("z", bf(2, 255), ValueError)):
+        with pytest.raises(error, match="o must be|is on cpu" if error is ValueError else name):
+            binding.grouped_out_proj_mxfp4(**dict(ok, **{name: value}))
+    with pytest.raises(ValueError, match="o is on cpu"):
+        binding.grouped_out_proj_mxfp4(**ok)
