@@ -402,6 +402,13 @@ CSA_DEV float2 add_f32x2(float2 a, float2 b) {
   return *reinterpret_cast<const float2*>(&d);
 }
 
+// The larger value, NaN where either is NaN (fmaxf drops it).
+CSA_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 CSA_DEV float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -260,10 +260,13 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
   }
   const float LOG2E = 1.4426950408889634f;
   const float z2 = z * LOG2E;  // log2 domain
-  float M = fmaxf(z2, m0);
-  for (int s = lane + 32; s < S; s += 32) M = fmaxf(M, src.maximum(s));
-  M = warp_max(M);
-  const bool zero = z == INFINITY || M == -INFINITY;  // +inf sink, or nothing to attend
+  // (A split with a NaN logit has a NaN maximum: it makes every weight NaN.)
+  float M = max_nan(z2, m0);
+  for (int s = lane + 32; s < S; s += 32) M = max_nan(M, src.maximum(s));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+  // +inf sink, or nothing to attend
+  const bool zero = (z == INFINITY && !isnan(M)) || M == -INFINITY;
   float L = 0.f;
   if (!zero) {
     for (int s = lane; s < S; s += 32) {
@@ -1162,8 +1165,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
           const float2 y = mul_f32x2(make_float2(sv[j], sv[j + 1]), sc2);
           sv[j] = y.x;
           sv[j + 1] = y.y;
-          m4[j & 3] = fmaxf(m4[j & 3], y.x);
-          m4[(j + 1) & 3] = fmaxf(m4[(j + 1) & 3], y.y);
+          m4[j & 3] = max_nan(m4[j & 3], y.x);
+          m4[(j + 1) & 3] = max_nan(m4[(j + 1) & 3], y.y);
         }
       } else {
 #pragma unroll
@@ -1172,15 +1175,18 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
           if (win) x *= M.rn[32 * hf + j];
           x = ((vw >> j) & 1u) ? x * p.scale_log2 : -INFINITY;
           sv[j] = x;
-          m4[j & 3] = fmaxf(m4[j & 3], x);
+          m4[j & 3] = max_nan(m4[j & 3], x);
         }
       }
-      float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));  // the row's other half
-      // Online softmax with lazy rescaling.
+      float mt = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+      mt = max_nan(mt, __shfl_xor_sync(0xffffffffu, mt, 16));  // the row's other half
+      // Online softmax with lazy rescaling.  The maximum of a row with a NaN
+      // logit is NaN from that tile on, and with it every weight, the sum and
+      // (rescaled) what O already holds: its maximum is never -infinity, which
+      // stands for a row without logits.
       constexpr float kGrow = kRescaleThreshold * 1.4426950408889634f + kWeightBias<kMx>;
-      const bool grow = mt > m_run + kGrow || m_run == -INFINITY;
-      const float m_new = grow ? fmaxf(kMx ? mt - kWeightBias<kMx> : mt, m_run) : m_run;
+      const bool grow = !(mt <= m_run + kGrow);  // (so where either is NaN)
+      const float m_new = grow ? max_nan(kMx ? mt - kWeightBias<kMx> : mt, m_run) : m_run;
       const bool need = grow && m_run != -INFINITY;
       // P buffer a was last read by P.V of tile it-2; rescaling O needs
       // every earlier P.V complete (the latest is tile it-1).  pvdone[x]
@@ -1292,8 +1298,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       bool zero = false;
       float ang_s = 0.f, ang_c = 1.f;
       if (p.fused) {
-        M = fmaxf(m_run, z2);
-        zero = zs == INFINITY || M == -INFINITY;
+        M = max_nan(m_run, z2);
+        zero = (zs == INFINITY && !isnan(M)) || M == -INFINITY;
         if (!zero) {
           const float wm = m_run == -INFINITY ? 0.f : exp2f(m_run - M);
           L = l_run * wm + (z2 == -INFINITY ? 0.f : exp2f(z2 - M));
