@@ -96,12 +96,14 @@ CSA_DEV void mx_values8(uint32_t w, uint32_t lo, uint32_t (&o)[4]) {
 // The same in fp16, the form the attention's tensor cores take.  fp16 holds the
 // codes and the factor 2^(s-127) of scale bytes 103 .. 142 (2^-24 .. 2^15): one
 // conversion and one exact product a pair.  Values are exact from s = 104 to
-// s = 140 (49152); a scale below 103 is zero; above 140 it overflows to
-// infinity or NaN (255: NaN), which the caller reports.
+// s = 140 (49152); a scale below 103 is zero.  Above 140 (where six times the
+// scale passes fp16's range) the factor is NaN, whatever the block's codes:
+// 255 is a NaN block, and an infinity could end as a weight of zero and be lost.
+// The caller reports 141 .. 254.
 constexpr uint32_t kMxF16Top = 140u;
 CSA_DEV uint32_t mx_f16_scale(uint32_t s) {
-  const float f = __uint_as_float(s << 23);  // 2^(s-127); 0 for s = 0, infinity for 255
-  return h2_bits(__floats2half2_rn(f, f));
+  const float f = __uint_as_float(s << 23);  // 2^(s-127); 0 for s = 0
+  return s > kMxF16Top ? 0x7FFF7FFFu : h2_bits(__floats2half2_rn(f, f));
 }
 CSA_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;

@@ -523,10 +523,11 @@ csa_status mxfp4_cache_read(const csa_params* p, const void* kv4, int64_t N_cap,
  *     104 .. 140 (2^-23 .. 2^13) are exact, those with 103 round to multiples
  *     of 2^-24, smaller ones are zeros, and a larger one is reported
  *     (CSA_ERR_UNSUPPORTED_SHAPE in dev_status) and makes its row's outputs
- *     infinite or NaN.  Gains up to 2048 in magnitude fit.  A softmax weight
+ *     NaN.  Gains up to 2048 in magnitude fit.  A softmax weight
  *     below 2^-18 of its row's largest is rounded by at most 2^-29 of that.
- *   - An entry that is NaN and is selected (or visible, dense) makes its
- *     row's outputs NaN; entries that are not selected are never read.
+ *   - An entry that is NaN (a scale byte of 255, whatever the codes) and is
+ *     selected (or visible, dense) makes its row's outputs NaN; entries that
+ *     are not selected are never read.
  *   - The indexer's keys are the E4M3 keys of the bf16 cache.
  * The context split below takes bf16 caches only. */
 csa_status hca_compress_mxfp4(const csa_params* p, const void* kv_tok, int64_t L_cap,

@@ -562,3 +562,24 @@ def test_hca_prefill_chunk(orc, P, T):
     ro, rl = orc.mqa(bits16(qi["q"]), (P + np.arange(T)).reshape(1, T), bits16(vals), bits16(kv_tok),
                      f32(qi["sink"]), m, w.W, w.rope_dim)
     assert_close(out, lse, ro[0], rl[0])
+
+
+@pytest.mark.parametrize("k", [0, 100])
+@pytest.mark.parametrize("B", [2, 150])  # several splits, one
+@pytest.mark.parametrize("byte,status", [(255, 0), (141, 2), (142, 2), (200, 2), (254, 2)])
+def test_scales_without_an_fp16_value_make_their_rows_nan(k, B, byte, status):
+    """A scale byte of 255 is a NaN block whatever its codes (here 0.5 .. 6 and
+    their negatives; the library itself writes zeros), and one above 140 is
+    reported; both make the row NaN in every dim, alone in its tile (entry 64
+    of 65, no window) or not."""
+    for n, e in ((65, 64), (65, 3), (1, 0)):
+        c = Case(B, 128, 20, 32, 0, 4, [4 * n - 1] * B, n, k=min(k, n))
+        ref = c.run(c.kv4)
+        b = B - 1
+        for codes in (0x11, 0xF1, 0x00):
+            bad = c.kv4.clone()
+            bad[b, e, 16:32] = codes
+            bad[b, e, 64 + 1] = byte
+            out, lse = c.run(bad, status=status)
+            assert torch.isnan(out[b].float()).all() and torch.isnan(lse[b]).all()
+            assert torch.equal(out[:b], ref[0][:b]) and torch.equal(lse[:b], ref[1][:b])
