@@ -4,9 +4,11 @@
 // microscaling formats), two codes a byte, the even value in the low nibble.
 //
 // Quantisation (of bf16 values): e is the smallest integer with
-// max|x| <= 6 * 2^e, so no value saturates; codes round x * 2^-e to nearest,
-// ties to even.  x * 2^-e is exact in fp32 and every rounding border is a
-// representable number, so codes and scales are defined bit for bit.
+// max|x| <= 6 * 2^e, at most 125, so that every code times 2^e is finite in
+// bf16 and no value saturates but those above 6 * 2^125 = 1.5 * 2^127; codes
+// round x * 2^-e to nearest, ties to even.  x * 2^-e is exact in fp32 and every
+// rounding border is a representable number, so codes and scales are defined bit
+// for bit.
 // Values (code * 2^e) are exact in bf16.
 #pragma once
 
@@ -20,11 +22,12 @@ constexpr int kMxBlock = 32;
 // Scale byte of a block from the bf16 bits (sign cleared) of its largest
 // magnitude.  amax = 1.f * 2^k <= 6 * 2^e = 1.5 * 2^(e+2): e = k - 2, one more
 // when the fraction exceeds one half.  0 for a zero block; 255 (NaN) when a
-// value is NaN or infinite.
+// value is NaN or infinite; otherwise at most 252 (e = 126 would turn finite
+// values into infinities: 4 * 2^126).
 CSA_DEV uint32_t mx_scale_byte(uint32_t amax) {
-  if (amax >= 0x7F80u) return 255u;
-  const int e = (int)(amax >> 7) - 2 + ((amax & 0x7Fu) > 0x40u ? 1 : 0);
-  return e > 0 ? (uint32_t)e : 0u;
+  // (63 carries into the exponent where the fraction exceeds one half.)
+  const int e = ((int)amax + 63 - 2 * 128) >> 7;
+  return amax >= 0x7F80u ? 255u : (uint32_t)__vimin_s32_relu(e, 252);
 }
 
 // Eight fp32 values (pairs) -> eight codes, value i in bits 4i.
@@ -44,8 +47,8 @@ CSA_DEV uint32_t mx_codes8(const float2 (&x)[4]) {
 
 // Eight bf16 values (pairs) of a block with scale byte `s` -> codes.
 CSA_DEV uint32_t mx_quantise8(const uint32_t (&w)[4], uint32_t s) {
-  // 2^(127 - s) brings the block into E2M1 range (s <= 253 for finite blocks).
-  const float f = __uint_as_float((254u - min(s, 253u)) << 23);
+  // 2^(127 - s) brings the block into E2M1 range (s <= 252 for finite blocks).
+  const float f = __uint_as_float((254u - min(s, 252u)) << 23);
   const float2 f2 = make_float2(f, f);
   float2 x[4];
 #pragma unroll

@@ -479,13 +479,14 @@ csa_status hca_prefill_chunk(const csa_params* p, int64_t P, int T, const void* 
  * mxfp4_row_bytes(512) = 272, mxfp4_row_bytes(128) = 80; 0 for other d.
  * A cache is kv4 [B, N_cap, mxfp4_row_bytes(d)] uint8 (device).
  *
- * Quantisation: e is the smallest integer (at least -127) with
- * max|x| <= 6 * 2^e, so no value saturates; codes round x / 2^e to nearest,
- * ties to the even code.  A block of zeros has the byte 0; a block that holds
- * a NaN or an infinity has the byte 255 and reads back as NaN.  The result
- * is defined bit for bit, and every stored value is exact in bf16.  Rows read
- * back and written again keep their values (not always their bytes: a block
- * whose largest value is 3 * 2^e takes the scale 2^(e-1)).
+ * Quantisation: e is the smallest integer (from -127 to 125) with
+ * max|x| <= 6 * 2^e, so no value up to 6 * 2^125 (2.55e38) saturates, and larger
+ * ones are stored as that; codes round x / 2^e to nearest, ties to the even
+ * code.  A block of zeros has the byte 0; a block that holds a NaN or an
+ * infinity has the byte 255 and reads back as NaN.  The result is defined bit
+ * for bit, and every stored value is exact in bf16.  Rows read back and written
+ * again keep their values (not always their bytes: a block whose largest value
+ * is 3 * 2^e takes the scale 2^(e-1)).
  *
  * mxfp4_cache_write: rows rows[b, i, :] (i < count[b], at most n) of sequence
  * b are quantised into entries first_entry[b] + i.  Other entries, and rows

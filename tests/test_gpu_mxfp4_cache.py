@@ -255,3 +255,29 @@ def test_calls_behind_copies_memsets_and_joined_streams():
     for _ in range(20):
         g.replay()
         check()
+
+
+def test_values_next_to_the_largest_stay_finite():
+    """Above 6 * 2^125 = 1.5 * 2^127 values are stored as that, not as infinity;
+    the scale byte stays at 252, the largest whose every code is finite in bf16."""
+    top = 1.5 * 2.0 ** 127
+    mags = torch.tensor([1.5, 1.5078125, 1.625, 1.75, 1.875, 1.9921875]).double() * 2.0 ** 127
+    rows = torch.zeros(1, len(mags), 128, dtype=torch.double)
+    rows[0, :, 3] = mags
+    rows[0, :, 40] = -mags
+    rows[0, :, 41] = 2.0 ** 125  # code 2: the block's other values keep their step
+    rows = rows.bfloat16().to(DEV)
+    assert torch.equal(rows[0, :, 3].double().cpu(), mags)
+    p = binding.make_params(1, 128)
+    kv4 = binding.mxfp4_cache(p, len(mags))
+    binding.mxfp4_cache_write(p, rows, kv4)
+    back = torch.empty_like(rows)
+    binding.mxfp4_cache_read(p, kv4, back)
+    codes, scales = binding.mxfp4_quantize(rows[0])
+    torch.cuda.synchronize()
+    want = torch.zeros(1, len(mags), 128, dtype=torch.double)
+    want[0, :, 3], want[0, :, 40], want[0, :, 41] = top, -top, 2.0 ** 125
+    assert torch.equal(back.double().cpu(), want)
+    assert kv4[0, :, 64].eq(252).all() and kv4[0, :, 65].eq(252).all()
+    assert torch.equal(codes, kv4[0, :, :64])
+    assert scales.view(32, 16)[: len(mags), :2].eq(252).all()
