@@ -329,6 +329,11 @@ CSA_DEV void tmem_st_16x32bx2_x32(uint32_t taddr, const uint32_t (&r)[32]) {
 // writes, and reads of anything a kernel of this library writes, come after
 // pdl_wait(); only reads of caller inputs and on-chip set-up come before.
 // pdl_trigger() lets the next kernel in the stream be scheduled early.
+//
+// A kernel that waits is resident while its predecessor still writes, so what
+// that may write is never read-only for the kernel's whole duration, which the
+// non-coherent path (__ldg, or a const __restrict__ pointer) requires: such data
+// is read with __ldcg or plain loads after the wait.
 CSA_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 CSA_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Every thread of a call's first kernel in head mode (see launch_pdl), before it

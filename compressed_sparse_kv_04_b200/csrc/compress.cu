@@ -89,7 +89,7 @@ CSA_DEV void load_row(const __nv_bfloat16* row, int lane, float (&x)[DIM / 32]) 
   for (int p = 0; p < LN::NPART; ++p) {
     const __nv_bfloat16* src = row + LN::elem(lane, p, 0);
     if constexpr (LN::VEC == 8) {
-      uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+      uint4 u = __ldcg(reinterpret_cast<const uint4*>(src));
       uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -97,13 +97,13 @@ CSA_DEV void load_row(const __nv_bfloat16* row, int lane, float (&x)[DIM / 32]) 
         x[p * 8 + 2 * q + 1] = bf16_hi(w[q]);
       }
     } else if constexpr (LN::VEC == 4) {
-      uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+      uint2 u = __ldcg(reinterpret_cast<const uint2*>(src));
       x[p * 4 + 0] = bf16_lo(u.x);
       x[p * 4 + 1] = bf16_hi(u.x);
       x[p * 4 + 2] = bf16_lo(u.y);
       x[p * 4 + 3] = bf16_hi(u.y);
     } else {
-      uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(src));
+      uint32_t u = __ldcg(reinterpret_cast<const uint32_t*>(src));
       x[p * 2 + 0] = bf16_lo(u);
       x[p * 2 + 1] = bf16_hi(u);
     }
@@ -118,17 +118,17 @@ CSA_DEV void load_row_packed(const __nv_bfloat16* row, int lane, uint32_t (&w)[D
   for (int p = 0; p < LN::NPART; ++p) {
     const __nv_bfloat16* src = row + LN::elem(lane, p, 0);
     if constexpr (LN::VEC == 8) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+      const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src));
       w[p * 4] = u.x;
       w[p * 4 + 1] = u.y;
       w[p * 4 + 2] = u.z;
       w[p * 4 + 3] = u.w;
     } else if constexpr (LN::VEC == 4) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+      const uint2 u = __ldcg(reinterpret_cast<const uint2*>(src));
       w[p * 2] = u.x;
       w[p * 2 + 1] = u.y;
     } else {
-      w[p] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      w[p] = __ldcg(reinterpret_cast<const uint32_t*>(src));
     }
   }
 }
@@ -149,7 +149,7 @@ CSA_DEV void pool_tokens(const __nv_bfloat16* blk, int j0, int j_load, int j_use
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   // The position biases of this warp's tokens (at most 32), one load per
   // lane up front instead of one dependent load per token.
-  const float bp = j0 + lane < j_use ? __ldg(b_pos + j0 + lane) : 0.f;
+  const float bp = j0 + lane < j_use ? b_pos[j0 + lane] : 0.f;
   for (int j = j0; j < j_load; j += RB) {
     uint32_t w[RB][E / 2];
 #pragma unroll
@@ -347,14 +347,14 @@ CSA_DEV void pool_stream(const PoolArgs& a, const StreamArgs& sa, float* smem) {
 #pragma unroll
   for (int part = 0; part < LN::NPART; ++part)
 #pragma unroll
-    for (int v = 0; v < LN::VEC; ++v) ws[part * LN::VEC + v] = __ldg(sa.w_s + LN::elem(lane, part, v));
+    for (int v = 0; v < LN::VEC; ++v) ws[part * LN::VEC + v] = sa.w_s[LN::elem(lane, part, v)];
   // The gains, loaded with the other inputs (used after the pooling).
   float gam[E];
 #pragma unroll
   for (int part = 0; part < LN::NPART; ++part)
 #pragma unroll
     for (int v = 0; v < LN::VEC; ++v)
-      gam[part * LN::VEC + v] = sa.gamma ? __ldg(sa.gamma + LN::elem(lane, part, v)) : 1.f;
+      gam[part * LN::VEC + v] = sa.gamma ? sa.gamma[LN::elem(lane, part, v)] : 1.f;
 
   // Row j of the window is blk + j*DIM (only rows j >= jlo are touched).
   const __nv_bfloat16* blk = sa.tok + ((int64_t)b * a.L_cap + gblk * a.m - a.overlap) * DIM;

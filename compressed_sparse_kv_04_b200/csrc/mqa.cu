@@ -201,17 +201,13 @@ struct Partials {
       : src(p.part_o + ((int64_t)row * p.splits * p.H + h) * D + part * (D / kParts) +
             lane * (D / kParts / 32)),
         ml(p.part_ml + (int64_t)row * p.splits * 2 * p.H + h), stride((int64_t)p.H * D), H(p.H) {}
-  template <typename T>
-  CSA_DEV static T ld(const T* a) {
-    return __ldg(a);
-  }
-  CSA_DEV float maximum(int s) const { return ld(ml + (int64_t)s * 2 * H); }
-  CSA_DEV float sum(int s) const { return ld(ml + (int64_t)s * 2 * H + H); }
+  CSA_DEV float maximum(int s) const { return ml[(int64_t)s * 2 * H]; }
+  CSA_DEV float sum(int s) const { return ml[(int64_t)s * 2 * H + H]; }
   CSA_DEV uint4 load16(int s) const {
-    return ld(reinterpret_cast<const uint4*>(src + (int64_t)s * stride));
+    return *reinterpret_cast<const uint4*>(src + (int64_t)s * stride);
   }
   CSA_DEV uint2 load8(int s) const {
-    return ld(reinterpret_cast<const uint2*>(src + (int64_t)s * stride));
+    return *reinterpret_cast<const uint2*>(src + (int64_t)s * stride);
   }
 };
 
@@ -248,16 +244,17 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
     else
       *reinterpret_cast<uint2*>(&v[0]) = src.load8(s);
   };
-  uint32_t buf[G][NW];
-#pragma unroll
-  for (int u = 0; u < G; ++u)
-    if (u < S) load(u, buf[u]);
-  // Split `lane`'s (max, sum) pair, in flight with the partials.
+  // Split `lane`'s (max, sum) pair first (its chain is the longer one), then the
+  // partials, all in flight together.
   float m0 = -INFINITY, l0 = 0.f;
   if (lane < S) {
     m0 = src.maximum(lane);
     l0 = src.sum(lane);
   }
+  uint32_t buf[G][NW];
+#pragma unroll
+  for (int u = 0; u < G; ++u)
+    if (u < S) load(u, buf[u]);
   const float LOG2E = 1.4426950408889634f;
   const float z2 = z * LOG2E;  // log2 domain
   // (A split with a NaN logit has a NaN maximum: it makes every weight NaN.)
@@ -348,8 +345,13 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
 // kernel has set itself up before the attention ends.
 template <int D>
 constexpr int kMergeParts = D / 128;
+// Groups of up to 16 are held to 72 registers: 8 rows of 128 heads are 1024 CTAs, and
+// seven on an SM take them in one wave (dense 8 x 8192 entries 37.6 us, 39.9 with 80
+// registers).  Larger groups merge few rows; there the registers of a lone CTA keep
+// all loads in flight (2 x 8192 entries 21.9 us, 22.3 with 128).
 template <int D, int R, int G>
-__global__ void __launch_bounds__(128) mqa_combine_kernel(const Params p, int rows) {
+__global__ void __launch_bounds__(128, G <= 16 ? 7 : 1)
+    mqa_combine_kernel(const Params p, int rows) {
   constexpr int kParts = kMergeParts<D>;
   extern __shared__ float wsm[];  // [4 warps][S] split weights
   pdl_trigger();
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     // and the KV gain in place.  Every real row: RoPE on the rotated dims.
     const int tid = threadIdx.x - 64;  // 0 .. NT-1
     const int r = tid >> 1, hf = tid & 1;
-    for (int i = tid; i < D; i += NT) gam_s[D + i] = p.gamma_kv ? __ldg(p.gamma_kv + i) : 1.f;
+    for (int i = tid; i < D; i += NT) gam_s[D + i] = p.gamma_kv ? p.gamma_kv[i] : 1.f;
     named_barrier_sync(2, NT);  // the transform warps
     if (sel_tiles) pdl_wait();  // selected rows are gathered here
     const int n_c = sel_tiles ? sel_count() : (p.sel_idx ? 0 : (int)n_vis);
@@ -1044,7 +1046,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     // all sit in the last 64-dim chunk of half 1.
     {
       for (int i = threadIdx.x - 32 * W0; i < D; i += 128)
-        gam_s[i] = p.gamma_q ? __ldg(p.gamma_q + i) : 1.f;
+        gam_s[i] = p.gamma_q ? p.gamma_q[i] : 1.f;
       named_barrier_sync(1, 128);  // the softmax warps
       // The block is in the last stage (TMA, 128-byte swizzled chunks):
       // row hl, dims [hf*D/2, hf*D/2 + D/2).

@@ -88,7 +88,7 @@ CSA_DEV void write_rows(const WriteArgs& a, const Range& rg) {
         live[u] = false;
       }
     }
-    v[u] = live[u] ? __ldg(reinterpret_cast<const uint4*>(src + u * C::kStep * (2 * D)))
+    v[u] = live[u] ? __ldcg(reinterpret_cast<const uint4*>(src + u * C::kStep * (2 * D)))
                    : make_uint4(0, 0, 0, 0);
   }
   uint8_t* row = a.cache + ((int64_t)b * a.n_cap + rg.first + i0) * kRow;
@@ -162,8 +162,8 @@ CSA_DEV void read_rows(const ReadArgs& a, const Range& rg) {
     codes[u] = s[u] = 0;
     if (live[u]) {
       const uint8_t* row = src + e * kRow;
-      codes[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * j));
-      s[u] = __ldg(row + D / 2 + j / 4);
+      codes[u] = __ldcg(reinterpret_cast<const uint32_t*>(row + 4 * j));
+      s[u] = __ldcg(row + D / 2 + j / 4);
     }
   }
 #pragma unroll

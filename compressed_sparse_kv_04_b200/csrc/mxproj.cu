@@ -683,10 +683,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // blockIdx.y: 128 rows, a warp per row: 512 bytes read and one full line of
 // codes written at a time.  The scale bytes of rows past the last one are
 // written as zeros.
-__global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* __restrict__ x,
-                                                          int64_t ld_bytes, int64_t rows,
-                                                          int64_t cols, uint8_t* codes,
-                                                          uint8_t* scales, int head) {
+__global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* x, int64_t ld_bytes,
+                                                          int64_t rows, int64_t cols,
+                                                          uint8_t* codes, uint8_t* scales,
+                                                          int head) {
   constexpr int kU = 8;  // rows in flight per warp
   if (head)
     pdl_head();
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(256) mx_quantise_kernel(const uint8_t* __restr
 #pragma unroll
     for (int u = 0; u < kU; ++u)
       v[u] = in && warp + g + 8 * u < live
-                 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(g + 8 * u) * ld_bytes))
+                 ? __ldcg(reinterpret_cast<const uint4*>(src + (int64_t)(g + 8 * u) * ld_bytes))
                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {

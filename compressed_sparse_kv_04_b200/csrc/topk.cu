@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_kernel(const Params p) {
   const int cap = (int)(p.N_cap - lo < p.slice ? (p.N_cap - lo > 0 ? p.N_cap - lo : 0) : p.slice);
   const float* src = p.scores + (int64_t)row * p.N_cap + lo;
 #pragma unroll 8
-  for (int i = tid; i < cap; i += kThreads) keys[i] = orderable(__ldg(src + i));
+  for (int i = tid; i < cap; i += kThreads) keys[i] = orderable(__ldcg(src + i));
   int64_t n = pos < 0 ? 0 : (pos + 1) / p.m - p.entry_offset;
   if (n < 0) n = 0;
   if (n > p.N_cap) {
@@ -624,14 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) topk_row_kernel(const Params p) {
   const int n4 = vec ? (n & ~3) : 0;
 #pragma unroll 4
   for (int i = 4 * tid; i < n4; i += 4 * kThreads) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(src + i));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
     const uint4 u = make_uint4(orderable(v.x), orderable(v.y), orderable(v.z), orderable(v.w));
     *reinterpret_cast<uint4*>(keys + i) = u;
     kmin = min(kmin, min(min(u.x, u.y), min(u.z, u.w)));
     kmax = max(kmax, max(max(u.x, u.y), max(u.z, u.w)));
   }
   for (int i = n4 + tid; i < n; i += kThreads) {
-    const uint32_t u = orderable(__ldg(src + i));
+    const uint32_t u = orderable(__ldcg(src + i));
     keys[i] = u;
     kmin = min(kmin, u);
     kmax = max(kmax, u);
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_hist_kernel(const Params p) 
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = wbase + 32 * j + lane;
-    sv[j] = (32 * j < ch && i < len) ? __ldg(src + i) : 0.f;
+    sv[j] = (32 * j < ch && i < len) ? __ldcg(src + i) : 0.f;
   }
 
   // b*: an exclusive scan over threads counts the scores in higher bins.
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_hist_kernel(const Params p) 
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = wbase + 32 * (j0 + j) + lane;
-        sv[j] = (32 * (j0 + j) < ch && i < len) ? __ldg(src + i) : 0.f;
+        sv[j] = (32 * (j0 + j) < ch && i < len) ? __ldcg(src + i) : 0.f;
       }
     }
 #pragma unroll
