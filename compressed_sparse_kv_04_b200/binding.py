@@ -9,6 +9,7 @@ library has not been built: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 import torch
@@ -187,6 +188,25 @@ def _ptr(t):
     return C.c_void_p(t.data_ptr())
 
 
+def _cache_ptr(p, kv_c):
+    """Address of a bf16 cache [B, N_cap, d], which has to hold its entries' bytes
+    (a 4-bit cache holds about a quarter of them: the calls would pass its end)."""
+    need = p.B * kv_c.shape[1] * p.d * 2
+    if kv_c.nbytes < need:
+        raise ValueError(f"kv_c holds {kv_c.nbytes} bytes, {p.B} x {kv_c.shape[1]} bf16 entries of "
+                         f"{p.d} take {need} (a 4-bit cache goes to the _mxfp4 calls)")
+    return _ptr(kv_c)
+
+
+def _weight_ptr(w, name, *shape):
+    """Address of a bf16 weight, which has to hold that many values' bytes."""
+    need = 2 * math.prod(shape)
+    if w.nbytes < need:
+        raise ValueError(f"{name} holds {w.nbytes} bytes, {list(shape)} in bf16 take {need} "
+                         "(4-bit weights go to grouped_out_proj_mxfp4)")
+    return _ptr(w)
+
+
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
@@ -219,7 +239,8 @@ def hca_compress(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, k
                  dev_status=None, stream=None):
     _check(lib().hca_compress(C.byref(p), _ptr(kv_tok), kv_tok.shape[1], _ptr(ctx_len),
                               _ptr(w_s), _ptr(b_pos), _ptr(gamma), first_block, n_blocks,
-                              _ptr(kv_c), kv_c.shape[1], _ptr(dev_status), _stream(stream)))
+                              _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(dev_status),
+                              _stream(stream)))
 
 
 def csa_compress(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv_c,
@@ -227,7 +248,7 @@ def csa_compress(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, k
                  dev_status=None, stream=None):
     _check(lib().csa_compress(C.byref(p), _ptr(kv_tok), kv_tok.shape[1], _ptr(ctx_len),
                               _ptr(w_s), _ptr(b_pos), _ptr(gamma), first_block, n_blocks,
-                              _ptr(kv_c), kv_c.shape[1], _ptr(idx_tok), _ptr(w_s_idx),
+                              _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(idx_tok), _ptr(w_s_idx),
                               _ptr(b_pos_idx), _ptr(idx_key), _ptr(idx_scale),
                               _ptr(dev_status), _stream(stream)))
 
@@ -278,7 +299,7 @@ def topk_select(p, Q, scores, pos_q, topk_idx, topk_cnt, dev_status=None, stream
 def sparse_mqa_decode(p, q, pos_q, kv_c, topk_idx, topk_cnt, kv_tok, sink, out, gamma_q=None,
                       gamma_kv=None, lse=None, ws=None, dev_status=None, stream=None):
     _check(lib().sparse_mqa_decode(
-        C.byref(p), _ptr(q), _ptr(pos_q), _ptr(kv_c), kv_c.shape[1], _ptr(topk_idx),
+        C.byref(p), _ptr(q), _ptr(pos_q), _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(topk_idx),
         _ptr(topk_cnt), _ptr(kv_tok), kv_tok.shape[1], _ptr(sink), _ptr(gamma_q),
         _ptr(gamma_kv), _ptr(out), _ptr(lse), _ptr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream)))
@@ -287,7 +308,7 @@ def sparse_mqa_decode(p, q, pos_q, kv_c, topk_idx, topk_cnt, kv_tok, sink, out, 
 def dense_mqa_decode(p, q, pos_q, kv_c, kv_tok, sink, out, gamma_q=None, gamma_kv=None,
                      lse=None, ws=None, dev_status=None, stream=None):
     _check(lib().dense_mqa_decode(
-        C.byref(p), _ptr(q), _ptr(pos_q), _ptr(kv_c), kv_c.shape[1], _ptr(kv_tok),
+        C.byref(p), _ptr(q), _ptr(pos_q), _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(kv_tok),
         kv_tok.shape[1], _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(out), _ptr(lse),
         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
         _stream(stream)))
@@ -298,9 +319,9 @@ def csa_prefill_chunk(p, P, T, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_po
                       gamma_q=None, gamma_kv=None, ws=None, dev_status=None, stream=None):
     _check(lib().csa_prefill_chunk(
         C.byref(p), P, T, _ptr(kv_tok), _ptr(idx_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos),
-        _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _ptr(kv_c), _ptr(idx_key), _ptr(idx_scale),
-        kv_c.shape[1], _ptr(q), _ptr(q_idx), _ptr(q_scale), _ptr(w), _ptr(sink), _ptr(gamma_q),
-        _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt), _ptr(out), _ptr(ws),
+        _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _cache_ptr(p, kv_c), _ptr(idx_key),
+        _ptr(idx_scale), kv_c.shape[1], _ptr(q), _ptr(q_idx), _ptr(q_scale), _ptr(w), _ptr(sink),
+        _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt), _ptr(out), _ptr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream)))
 
 
@@ -310,8 +331,8 @@ def hca_prefill_chunk(p, P, T, kv_tok, w_s, b_pos, gamma, kv_c, q, sink, out, ga
     MQA per new query.  kv_tok [1, L_cap, d]; kv_c [1, N_cap, d]; q/out [T, H, d]."""
     _check(lib().hca_prefill_chunk(
         C.byref(p), P, T, _ptr(kv_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos), _ptr(gamma),
-        _ptr(kv_c), kv_c.shape[1], _ptr(q), _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(out),
-        _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(q), _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv),
+        _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         _ptr(dev_status), _stream(stream)))
 
 
@@ -322,9 +343,9 @@ def csa_decode_step(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos
     MQA) for B sequences at positions pos_q [B]."""
     _check(lib().csa_decode_step(
         C.byref(p), _ptr(pos_q), _ptr(kv_tok), _ptr(idx_tok), kv_tok.shape[1], _ptr(w_s),
-        _ptr(b_pos), _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _ptr(kv_c), _ptr(idx_key),
-        _ptr(idx_scale), kv_c.shape[1], _ptr(q), _ptr(q_idx), _ptr(q_scale), _ptr(w), _ptr(sink),
-        _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt), _ptr(out), _ptr(lse),
+        _ptr(b_pos), _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _cache_ptr(p, kv_c),
+        _ptr(idx_key), _ptr(idx_scale), kv_c.shape[1], _ptr(q), _ptr(q_idx), _ptr(q_scale),
+        _ptr(w), _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt), _ptr(out), _ptr(lse),
         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
         _stream(stream)))
 
@@ -340,14 +361,15 @@ class CsaDecodeStep:
     def __init__(self, p, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv_c, idx_key,
                  idx_scale, sink, topk_idx, topk_cnt, ws, gamma_q=None, gamma_kv=None,
                  dev_status=None):
-        self._fn = (lib().csa_decode_step_mxfp4 if _is_mxfp4(p, kv_c, kv_tok)
-                    else lib().csa_decode_step)
+        mx = _is_mxfp4(p, kv_c, kv_tok)
+        self._fn = lib().csa_decode_step_mxfp4 if mx else lib().csa_decode_step
         self._keep = (p, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos_idx, kv_c, idx_key,
                       idx_scale, sink, topk_idx, topk_cnt, ws, gamma_q, gamma_kv, dev_status)
         self._head = (C.byref(p),)
         self._mid = (_ptr(kv_tok), _ptr(idx_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos),
-                     _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _ptr(kv_c), _ptr(idx_key),
-                     _ptr(idx_scale), kv_c.shape[1])
+                     _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx),
+                     _ptr(kv_c) if mx else _cache_ptr(p, kv_c), _ptr(idx_key), _ptr(idx_scale),
+                     kv_c.shape[1])
         self._sink = (_ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt))
         self._tail = (_ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status))
 
@@ -376,12 +398,12 @@ class HcaDecodeStep:
 
     def __init__(self, p, kv_tok, w_s, b_pos, gamma, kv_c, sink, ws, gamma_q=None, gamma_kv=None,
                  dev_status=None):
-        self._fn = (lib().hca_decode_step_mxfp4 if _is_mxfp4(p, kv_c, kv_tok)
-                    else lib().hca_decode_step)
+        mx = _is_mxfp4(p, kv_c, kv_tok)
+        self._fn = lib().hca_decode_step_mxfp4 if mx else lib().hca_decode_step
         self._keep = (p, kv_tok, w_s, b_pos, gamma, kv_c, sink, ws, gamma_q, gamma_kv, dev_status)
         self._head = (C.byref(p),)
         self._mid = (_ptr(kv_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos), _ptr(gamma),
-                     _ptr(kv_c), kv_c.shape[1])
+                     _ptr(kv_c) if mx else _cache_ptr(p, kv_c), kv_c.shape[1])
         self._gains = (_ptr(sink), _ptr(gamma_q), _ptr(gamma_kv))
         self._tail = (_ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status))
 
@@ -454,7 +476,7 @@ def hca_decode_step(p, pos_q, kv_tok, w_s, b_pos, gamma, kv_c, q, sink, out, gam
     sequences at positions pos_q [B]."""
     _check(lib().hca_decode_step(
         C.byref(p), _ptr(pos_q), _ptr(kv_tok), kv_tok.shape[1], _ptr(w_s), _ptr(b_pos),
-        _ptr(gamma), _ptr(kv_c), kv_c.shape[1], _ptr(q), _ptr(sink), _ptr(gamma_q),
+        _ptr(gamma), _cache_ptr(p, kv_c), kv_c.shape[1], _ptr(q), _ptr(sink), _ptr(gamma_q),
         _ptr(gamma_kv), _ptr(out), _ptr(lse), _ptr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status), _stream(stream)))
 
@@ -476,9 +498,11 @@ def grouped_out_proj(o, w_g, w_o, z, y=None, ws=None, dev_status=None, stream=No
     if ws is None:
         ws = torch.empty(grouped_out_proj_workspace_bytes(T, H, D, g, d_g, d_model),
                          dtype=torch.uint8, device=o.device)
-    _check(lib().grouped_out_proj(T, H, D, g, d_g, d_model, _ptr(o), _ptr(w_g), _ptr(w_o),
-                                  _ptr(y), _ptr(z), _ptr(ws), ws.numel() * ws.element_size(),
-                                  _ptr(dev_status), _stream(stream)))
+    _check(lib().grouped_out_proj(T, H, D, g, d_g, d_model, _ptr(o),
+                                  _weight_ptr(w_g, "w_g", g, d_g, H // max(g, 1) * D),
+                                  _weight_ptr(w_o, "w_o", d_model, g * d_g), _ptr(y), _ptr(z),
+                                  _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status),
+                                  _stream(stream)))
 
 
 # -------------------------------------------------------------- 4-bit (MXFP4) cache --
@@ -822,7 +846,7 @@ def csa_merge_candidates(p, Q, G, cand_score, cand_idx, cand_cnt, N_cap, topk_id
 
 def sparse_mqa_partials(p, splits, q, pos_q, kv_c, topk_idx, topk_cnt, kv_tok, part_o, part_ml,
                         gamma_q=None, gamma_kv=None, dev_status=None, stream=None):
-    _check(lib().sparse_mqa_partials(C.byref(p), splits, _ptr(q), _ptr(pos_q), _ptr(kv_c),
+    _check(lib().sparse_mqa_partials(C.byref(p), splits, _ptr(q), _ptr(pos_q), _cache_ptr(p, kv_c),
                                      kv_c.shape[1], _ptr(topk_idx), _ptr(topk_cnt), _ptr(kv_tok),
                                      kv_tok.shape[1], _ptr(gamma_q), _ptr(gamma_kv),
                                      _ptr(part_o), _ptr(part_ml), _ptr(dev_status),

@@ -217,3 +217,77 @@ def test_native_projection_checks_every_argument():
             binding.grouped_out_proj_mxfp4(**dict(ok, **{name: value}))
     with pytest.raises(ValueError, match="o is on cpu"):
         binding.grouped_out_proj_mxfp4(**ok)
+
+
+class _FakeLib:
+    """Every entry point returns success and is noted."""
+
+    def __init__(self):
+        self.reached = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.reached.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The binding over a library that does nothing, tensors taken wherever they are."""
+    lib = _FakeLib()
+    monkeypatch.setattr(binding, "lib", lambda: lib)
+    monkeypatch.setattr(binding, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(binding, "_stream", lambda stream=None: None)
+    return lib
+
+
+def _bf16_cache_calls(p, c):
+    """Every call of the binding that takes a bf16 cache, on cache c."""
+    x = torch.zeros(2, 9, 4)
+    return {
+        "hca_compress": lambda: binding.hca_compress(p, x, x, x, x, x, 0, 1, c),
+        "csa_compress": lambda: binding.csa_compress(p, x, x, x, x, x, 0, 1, c),
+        "sparse_mqa_decode": lambda: binding.sparse_mqa_decode(p, x, x, c, x, x, x, x, x),
+        "dense_mqa_decode": lambda: binding.dense_mqa_decode(p, x, x, c, x, x, x),
+        "csa_prefill_chunk": lambda: binding.csa_prefill_chunk(p, 0, 1, *[x] * 7, c, *[x] * 10),
+        "hca_prefill_chunk": lambda: binding.hca_prefill_chunk(p, 0, 1, *[x] * 4, c, x, x, x),
+        "csa_decode_step": lambda: binding.csa_decode_step(p, *[x] * 8, c, *[x] * 10),
+        "hca_decode_step": lambda: binding.hca_decode_step(p, *[x] * 5, c, x, x, x),
+        "sparse_mqa_partials": lambda: binding.sparse_mqa_partials(p, 1, x, x, c, *[x] * 5),
+    }
+
+
+def test_calls_on_bf16_caches_refuse_one_that_is_too_short(fake):
+    """A 4-bit cache holds about a quarter of a bf16 cache's bytes: such a call
+    would read and write past its end.  Refused before the library is reached."""
+    p = P(B=2, k=8)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    for bad in (torch.zeros(2, 8, 272, dtype=torch.uint8), bf(2, 8, 511), bf(1, 8, 512)):
+        for name, call in _bf16_cache_calls(p, bad).items():
+            with pytest.raises(ValueError, match="kv_c holds"):
+                call()
+    assert fake.reached == []
+    for name, call in _bf16_cache_calls(p, bf(2, 8, 512)).items():
+        call()
+    assert fake.reached == list(_bf16_cache_calls(p, None))
+
+
+def test_prepared_steps_refuse_a_bf16_cache_that_is_too_short(fake):
+    x, bad = torch.zeros(2, 9, 4), torch.zeros(1, 8, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="kv_c holds"):
+        binding.CsaDecodeStep(P(B=2), *[x] * 7, bad, *[x] * 6)
+    with pytest.raises(ValueError, match="kv_c holds"):
+        binding.HcaDecodeStep(P(B=2), *[x] * 4, bad, x, x)
+
+
+def test_bf16_projection_refuses_4bit_weights(fake):
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    o, w_g, w_o, z, ws = bf(2, 4, 128), bf(2, 128, 256), bf(256, 256), bf(2, 256), u8(64)
+    for bad in (dict(w_g=u8(2, 128, 128)), dict(w_o=u8(256, 128))):
+        with pytest.raises(ValueError, match="mxfp4"):
+            binding.grouped_out_proj(**dict(dict(o=o, w_g=w_g, w_o=w_o, z=z, ws=ws), **bad))
+    assert fake.reached == []
+    binding.grouped_out_proj(o, w_g, w_o, z, ws=ws)
+    assert fake.reached == ["grouped_out_proj"]
