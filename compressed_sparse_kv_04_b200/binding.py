@@ -351,7 +351,7 @@ def csa_decode_step(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos
 
 
 class CsaDecodeStep:
-    """csa_decode_step (or, with a uint8 cache, csa_decode_step_mxfp4) for a
+    """csa_decode_step (or, with a 4-bit cache, csa_decode_step_mxfp4) for a
     fixed set of sequences: the arguments that stay the same from step to step
     (token buffers, caches, weights, sink and gains, the selection outputs,
     workspace and status word) are checked and converted once; each call
@@ -393,7 +393,7 @@ class CsaDecodeStep:
 
 
 class HcaDecodeStep:
-    """hca_decode_step (or, with a uint8 cache, hca_decode_step_mxfp4) for a
+    """hca_decode_step (or, with a 4-bit cache, hca_decode_step_mxfp4) for a
     fixed set of sequences (see CsaDecodeStep)."""
 
     def __init__(self, p, kv_tok, w_s, b_pos, gamma, kv_c, sink, ws, gamma_q=None, gamma_kv=None,
@@ -591,9 +591,11 @@ def _raw_stream(dev, stream):
 
 
 def _is_mxfp4(p, kv_c, kv_tok):
-    dev = _device()
-    if kv_c.dtype != torch.uint8:
+    """Whether a prepared step's cache is a 4-bit one: uint8 rows of that format's
+    width (bytes of any other width are a bf16 cache's)."""
+    if kv_c.dtype != torch.uint8 or kv_c.shape[-1] != lib().mxfp4_row_bytes(p.d):
         return False
+    dev = _device()
     _need_cache(dev, p, kv_c)
     _need_tok(dev, p, kv_tok)
     return True

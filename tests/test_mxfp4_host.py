@@ -291,3 +291,19 @@ def test_bf16_projection_refuses_4bit_weights(fake):
     assert fake.reached == []
     binding.grouped_out_proj(o, w_g, w_o, z, ws=ws)
     assert fake.reached == ["grouped_out_proj"]
+
+
+def test_prepared_steps_take_a_bf16_cache_as_bytes(monkeypatch):
+    """uint8 rows of d * 2 bytes are a bf16 cache, as before there were 4-bit
+    ones; uint8 rows of the 4-bit width go to the 4-bit step."""
+    monkeypatch.setattr(binding, "_ptr", lambda t: None if t is None else t.data_ptr())
+    tok, x = torch.zeros(2, 9, 512, dtype=torch.bfloat16), torch.zeros(2, 9, 4)
+    as_bytes = torch.zeros(2, 8, 512, dtype=torch.bfloat16).view(torch.uint8)
+    csa = binding.CsaDecodeStep(P(B=2), tok, *[x] * 6, as_bytes, *[x] * 6)
+    hca = binding.HcaDecodeStep(P(B=2), tok, *[x] * 3, as_bytes, x, x)
+    assert csa._fn is binding.lib().csa_decode_step
+    assert hca._fn is binding.lib().hca_decode_step
+    with pytest.raises(ValueError, match="kv4 is on cpu"):
+        binding.HcaDecodeStep(P(B=2), tok, *[x] * 3, torch.zeros(2, 8, 272, dtype=torch.uint8), x, x)
+    with pytest.raises(ValueError, match="kv_c holds"):
+        binding.HcaDecodeStep(P(B=2), tok, *[x] * 3, torch.zeros(2, 8, 80, dtype=torch.uint8), x, x)
