@@ -232,7 +232,7 @@ def workspace(p, op, Q, N_cap, device=None):
     """A zero-filled workspace (the decode step's score histogram starts
     cleared; each call leaves it so)."""
     return torch.zeros(workspace_bytes(p, op, Q, N_cap), dtype=torch.uint8,
-                       device=device or torch.cuda.current_device())
+                       device=torch.cuda.current_device() if device is None else device)
 
 
 def hca_compress(p, kv_tok, ctx_len, w_s, b_pos, gamma, first_block, n_blocks, kv_c,
@@ -518,7 +518,7 @@ def mxfp4_row_bytes(d):
 def mxfp4_cache(p, N_cap, device=None):
     """An empty (all zero) 4-bit cache [B, N_cap, row bytes] for these params."""
     return torch.zeros(p.B, N_cap, mxfp4_row_bytes(p.d), dtype=torch.uint8,
-                       device=device or torch.cuda.current_device())
+                       device=torch.cuda.current_device() if device is None else device)
 
 
 _ROW_BYTES = {}

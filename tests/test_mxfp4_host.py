@@ -307,3 +307,14 @@ def test_prepared_steps_take_a_bf16_cache_as_bytes(monkeypatch):
         binding.HcaDecodeStep(P(B=2), tok, *[x] * 3, torch.zeros(2, 8, 272, dtype=torch.uint8), x, x)
     with pytest.raises(ValueError, match="kv_c holds"):
         binding.HcaDecodeStep(P(B=2), tok, *[x] * 3, torch.zeros(2, 8, 80, dtype=torch.uint8), x, x)
+
+
+def test_allocations_honour_device_zero(monkeypatch):
+    """device=0 means device 0 where another device is current."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    placed = []
+    monkeypatch.setattr(torch, "zeros", lambda *s, dtype=None, device=None: placed.append(device))
+    for device in (0, "cuda:2", None):
+        binding.mxfp4_cache(P(), 8, device=device)
+        binding.workspace(P(), binding.OP_DENSE_MQA, 1, 8, device=device)
+    assert placed == [0, 0, "cuda:2", "cuda:2", 1, 1]
