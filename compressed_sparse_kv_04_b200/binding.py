@@ -345,8 +345,8 @@ def csa_decode_step(p, pos_q, kv_tok, idx_tok, w_s, b_pos, gamma, w_s_idx, b_pos
         C.byref(p), _ptr(pos_q), _ptr(kv_tok), _ptr(idx_tok), kv_tok.shape[1], _ptr(w_s),
         _ptr(b_pos), _ptr(gamma), _ptr(w_s_idx), _ptr(b_pos_idx), _cache_ptr(p, kv_c),
         _ptr(idx_key), _ptr(idx_scale), kv_c.shape[1], _ptr(q), _ptr(q_idx), _ptr(q_scale),
-        _ptr(w), _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt), _ptr(out), _ptr(lse),
-        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
+        _ptr(w), _ptr(sink), _ptr(gamma_q), _ptr(gamma_kv), _ptr(topk_idx), _ptr(topk_cnt),
+        _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
         _stream(stream)))
 
 

@@ -1,11 +1,14 @@
 """Build libcsa.so in-tree for sm_100a (nvcc, one object per .cu, then link)
-and _calls.so, the binding's native calls (g++, against torch's headers).
+and _calls.so, the binding's native calls (g++, against torch's and Python's
+headers).  libcsa.so needs nvcc alone: where torch or Python's headers are
+missing, or _calls.so does not compile, it is built all the same.
 
     python -m compressed_sparse_kv_04_b200.build [--force]
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
@@ -29,8 +32,20 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [HEADER]
+def _lib_deps():
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)
+            if os.path.join(CSRC, f) != CALLS_SRC] + [HEADER]
+
+
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(
+        os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def can_build_calls() -> bool:
+    """Whether what _calls.so compiles against is here."""
+    return importlib.util.find_spec("torch") is not None and os.path.exists(
+        os.path.join(sysconfig.get_paths()["include"], "Python.h"))
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -61,22 +76,22 @@ def _compile_calls() -> None:
     os.replace(tmp, CALLS)
 
 
+def lib_up_to_date() -> bool:
+    return _newer(LIB, _lib_deps())
+
+
+def calls_up_to_date() -> bool:
+    return _newer(CALLS, [CALLS_SRC, HEADER])
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return lib_up_to_date() and (calls_up_to_date() or not can_build_calls())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_lib(verbose: bool) -> None:
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        calls = ex.submit(_compile_calls)
         results = list(ex.map(_compile, srcs))
-        calls.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -86,6 +101,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
            "-lcudart"]
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = None
+        if not can_build_calls():
+            sys.stderr.write("_calls.so is not built: it needs torch and Python's headers\n")
+        elif force or not calls_up_to_date():
+            calls = ex.submit(_compile_calls)
+        if force or not lib_up_to_date():
+            _build_lib(verbose)
+        if calls is not None:
+            calls.result()  # (libcsa.so is in place by now)
     return LIB
 
 
