@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcsa.so")
 
@@ -85,6 +87,10 @@ def _native():
         except ImportError as e:
             raise RuntimeError("_calls.so not found or not loadable; build it with "
                                "`python -m compressed_sparse_kv_04_b200.build`") from e
+        if m.built_for != build.calls_tag():
+            raise RuntimeError(f"_calls.so was built for {m.built_for}, this is "
+                               f"{build.calls_tag()}; build it again with "
+                               "`python -m compressed_sparse_kv_04_b200.build`")
         m.bind(*(C.cast(f, C.c_void_p).value for f in (
             L.mxfp4_row_bytes, L.mxfp4_cache_write, L.mxfp4_cache_read,
             L.sparse_mqa_decode_mxfp4, L.dense_mqa_decode_mxfp4, L.grouped_out_proj_mxfp4)))

@@ -21,6 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcsa.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_TAG = os.path.join(BUILD, "calls.tag")  # what _calls.so was built for
 HEADER = os.path.join(ROOT, "include", "csa.h")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -59,12 +60,22 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def calls_tag() -> str:
+    """What _calls.so depends on besides its sources: it is compiled against one
+    torch's C++ types and one Python's."""
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('SOABI')}")
+
+
 def _compile_calls() -> None:
     import torch
     t = os.path.dirname(torch.__file__)
     tmp = CALLS + ".tmp"
+    tag = calls_tag()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DCSA_CALLS_TAG="{tag}"',
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), CALLS_SRC,
@@ -74,6 +85,8 @@ def _compile_calls() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_TAG, "w") as f:
+        f.write(tag)
 
 
 def lib_up_to_date() -> bool:
@@ -81,11 +94,14 @@ def lib_up_to_date() -> bool:
 
 
 def calls_up_to_date() -> bool:
-    return _newer(CALLS, [CALLS_SRC, HEADER])
+    if not _newer(CALLS, [CALLS_SRC, HEADER]) or not os.path.exists(CALLS_TAG):
+        return False
+    with open(CALLS_TAG) as f:
+        return f.read() == calls_tag()
 
 
 def up_to_date() -> bool:
-    return lib_up_to_date() and (calls_up_to_date() or not can_build_calls())
+    return lib_up_to_date() and (not can_build_calls() or calls_up_to_date())
 
 
 def _build_lib(verbose: bool) -> None:

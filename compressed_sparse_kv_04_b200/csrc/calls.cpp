@@ -369,4 +369,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+// built_for: the torch and Python whose headers this module was compiled against
+// (the build passes it); the binding refuses it under others.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", CSA_CALLS_TAG) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

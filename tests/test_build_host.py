@@ -3,13 +3,15 @@ import os
 
 import pytest
 
+from compressed_sparse_kv_04_b200 import binding
 from compressed_sparse_kv_04_b200 import build as csa_build
 
 
 @pytest.fixture
 def built(monkeypatch, tmp_path):
     """The build in an empty folder, with compilers that only leave their file."""
-    for name, file in (("BUILD", "_build"), ("LIB", "libcsa.so"), ("CALLS", "_calls.so")):
+    for name, file in (("BUILD", "_build"), ("LIB", "libcsa.so"), ("CALLS", "_calls.so"),
+                       ("CALLS_TAG", "calls.tag")):
         monkeypatch.setattr(csa_build, name, str(tmp_path / file))
     monkeypatch.setattr(csa_build, "_compile", lambda src: (src + ".o", ""))
 
@@ -52,6 +54,7 @@ def test_each_target_follows_its_own_sources(built, monkeypatch):
     def calls():
         made.append("calls")
         open(csa_build.CALLS, "w").close()
+        open(csa_build.CALLS_TAG, "w").write(csa_build.calls_tag())
     monkeypatch.setattr(csa_build, "_compile_calls", calls)
     monkeypatch.setattr(csa_build, "_compile", lambda src: (made.append("lib"), "")[::-1])
     csa_build.build()
@@ -65,3 +68,26 @@ def test_each_target_follows_its_own_sources(built, monkeypatch):
     os.utime(csa_build.LIB, (0, 0))
     csa_build.build()
     assert set(made) == {"lib"}
+
+
+def test_native_calls_of_another_torch_or_python_are_rebuilt(built, monkeypatch):
+    monkeypatch.setattr(csa_build, "_compile_calls", lambda: None)
+    csa_build.build()
+    open(csa_build.CALLS, "w").close()
+    assert not csa_build.calls_up_to_date()  # built by nobody knows what
+    open(csa_build.CALLS_TAG, "w").write(csa_build.calls_tag())
+    assert csa_build.up_to_date()
+    for other in ("torch 2.99, C++11 ABI 1, Python cpython-312-x86_64-linux-gnu",
+                  csa_build.calls_tag().replace("cpython-3", "cpython-4")):
+        monkeypatch.setattr(csa_build, "calls_tag", lambda: other)
+        assert not csa_build.up_to_date()
+
+
+def test_the_binding_refuses_native_calls_of_another_torch(monkeypatch):
+    csa_build.build()
+    monkeypatch.setattr(binding, "_calls", None)
+    assert binding._native().built_for == csa_build.calls_tag()
+    monkeypatch.setattr(binding, "_calls", None)
+    monkeypatch.setattr(csa_build, "calls_tag", lambda: "torch 2.99")
+    with pytest.raises(RuntimeError, match="built for .* this is torch 2.99"):
+        binding._native()
