@@ -98,7 +98,6 @@ struct MCfg {
 };
 
 struct Meta {
-  int32_t grow[TN];   // row coordinate in the tensor map
   int32_t pos[TN];    // RoPE position
   float rn[TN];       // window tokens: 1/rms(c_t); compressed entries: 1
   uint32_t valid[2];  // bit r: row r holds a real KV vector
@@ -182,9 +181,8 @@ CSA_DEV int64_t row_pos(const Params& p, int row) {
   return p.pos_q ? p.pos_q[row] : p.pos_base + row % p.Q;
 }
 
-template <bool kCluster = false>
 CSA_DEV bool wait_all(uint64_t* bar, uint32_t parity, const Params& p, volatile int* abort_flag) {
-  bool ok = mbar_wait<kCluster>(bar, parity, p.status, abort_flag);
+  bool ok = mbar_wait(bar, parity, p.status, abort_flag);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -587,7 +585,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       const bool win = t >= tiles_c;
       // Tiles that the transform warps fetch (every MXFP4 entry tile).
       const bool gathered = !win && (kMx || p.sel_idx != nullptr);
-      int32_t grow[2], rpos[2];
+      int32_t rpos[2], y0 = 0;  // y0: row 0's coordinate in the tensor map
       bool valid[2];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
             }
           }
           if (!valid[hh] && gathered) i = 0;
-          grow[hh] = (int32_t)((int64_t)b * p.N_cap + i);
+          if (hh == 0) y0 = (int32_t)((int64_t)b * p.N_cap + i);
           rpos[hh] = (int32_t)((i + 1) * p.m - 1);
         } else {
           const int j = (t - tiles_c) * TN + r;
@@ -614,7 +612,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
             valid[hh] = false;
           }
           const int64_t tok = w0 + j;
-          grow[hh] = (int32_t)((int64_t)b * p.L_cap + tok);
+          if (hh == 0) y0 = (int32_t)((int64_t)b * p.L_cap + tok);
           rpos[hh] = (int32_t)tok;
         }
       }
@@ -622,8 +620,6 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       const uint32_t vb1 = __ballot_sync(0xffffffffu, valid[1]);
       if (!wait_all(&empty[s], ph ^ 1, p, abort_flag)) break;
       Meta& M = meta[s];
-      M.grow[lane] = grow[0];
-      M.grow[lane + 32] = grow[1];
       M.pos[lane] = rpos[0];
       M.pos[lane + 32] = rpos[1];
       if (lane == 0) {
@@ -637,10 +633,10 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       }
       __syncwarp();
       if (!gathered) {
-        // Rows grow[0] .. grow[0]+63 are consecutive (rows past the list are
-        // fetched too and masked; rows past the tensor are zero-filled).
+        // 64 consecutive rows (rows past the list are fetched too and masked;
+        // rows past the tensor are zero-filled).
         uint8_t* dst = stages + s * C::kStageBytes;
-        const int32_t y0 = __shfl_sync(0xffffffffu, grow[0], 0);
+        y0 = __shfl_sync(0xffffffffu, y0, 0);
         if (lane < C::NC)
           tma_load_2d(dst + lane * C::kChunkBytes, win ? &box_t : &box_c, &full[s],
                       (int32_t)(lane * 64), y0);
@@ -716,47 +712,6 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     named_barrier_sync(2, NT);  // the transform warps
     if (sel_tiles) pdl_wait();  // selected rows are gathered here
     const int n_c = sel_tiles ? sel_count() : (p.sel_idx ? 0 : (int)n_vis);
-    // Tile `it`: selected entries are fetched here (thread pair r gathers
-    // row r, half hf each, 16 bytes per cp.async) once the stage is free;
-    // every thread then arrives on full[s] (after its copies land).
-    // Gathers: transform warp tw copies rows tw, tw+4, ..., tw+60 of the
-    // tile, a whole row per pair of instructions (lane l: 16 bytes at
-    // 16*l and 512+16*l), so each instruction reads 512 contiguous bytes.
-    // Lane l (< 16) holds the index of row tw + 4*l, loaded ahead.
-    const int tw = tid >> 5, tl = tid & 31;
-    auto row_index = [&](int it) -> int64_t {
-      const int t = t0 + it, j = t * TN + tw + 4 * (tl & 15);
-      return (p.sel_idx && t < tiles_c && j < p.kmax) ? (int64_t)p.sel_idx[(int64_t)row * p.kmax + j]
-                                                       : 0;
-    };
-    auto fetch = [&](int it, int64_t i) -> bool {
-      const int s = it % C::kStages;
-      const int t = t0 + it;
-      if (p.sel_idx != nullptr && t < tiles_c) {
-        const int j = t * TN + tw + 4 * (tl & 15);
-        if (j >= n_c || i < 0 || i >= n_vis) i = -1;  // masked row: not fetched (zeroed later)
-        if (!wait_all(&empty[s], ((it / C::kStages) & 1) ^ 1, p, abort_flag)) return false;
-        if (it == C::kStages - 1 && !wait_all(qready, 0, p, abort_flag)) return false;
-        uint8_t* st = stages + s * C::kStageBytes;
-        constexpr int kUnits = D / 8;  // 16-byte units per row
-#pragma unroll 4
-        for (int u = 0; u < TN / 4; ++u) {
-          const int64_t iu = __shfl_sync(0xffffffffu, i, u);
-          if (iu < 0) continue;
-          const int rr = tw + 4 * u;
-          const __nv_bfloat16* src = p.kv_c + ((int64_t)b * p.N_cap + iu) * D;
-#pragma unroll
-          for (int h = 0; h < (kUnits + 31) / 32; ++h) {
-            const int unit = 32 * h + tl;
-            if (unit < kUnits) cp_async_16(st + tile_off(rr, 8 * unit), src + 8 * unit);
-          }
-        }
-        cp_async_arrive(&full[s]);
-      } else {
-        mbar_arrive(&full[s]);
-      }
-      return true;
-    };
     // Window tokens of an MXFP4 call, four threads a row: raw bf16 rows ->
     // normalised, rotated, rounded once to fp16 (in place: a thread reads and
     // writes the same 16-byte units).  Shared memory bandwidth bounds it: with
@@ -1008,26 +963,67 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         }
       }
     } else {
-    constexpr int kAhead = C::kStages - 1;
-    bool fetch_ok = true;
-    {
-      int64_t ri[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) ri[u] = u < ntile ? row_index(u) : 0;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (u < ntile && fetch_ok) fetch_ok = fetch(u, ri[u]);
-    }
-    int64_t nxt = kAhead < ntile ? row_index(kAhead) : 0;
-    for (int it = 0; it < ntile && fetch_ok; ++it) {
-      if (!transform(it)) break;
-      if (it + kAhead < ntile) {
-        const int64_t cur = nxt;
-        if (it + kAhead + 1 < ntile) nxt = row_index(it + kAhead + 1);
-        fetch_ok = fetch(it + kAhead, cur);
+      // Tile `it`: selected entries are fetched here (thread pair r gathers
+      // row r, half hf each, 16 bytes per cp.async) once the stage is free;
+      // every thread then arrives on full[s] (after its copies land).
+      // Gathers: transform warp tw copies rows tw, tw+4, ..., tw+60 of the
+      // tile, a whole row per pair of instructions (lane l: 16 bytes at
+      // 16*l and 512+16*l), so each instruction reads 512 contiguous bytes.
+      // Lane l (< 16) holds the index of row tw + 4*l, loaded ahead.
+      const int tw = tid >> 5, tl = tid & 31;
+      auto row_index = [&](int it) -> int64_t {
+        const int t = t0 + it, j = t * TN + tw + 4 * (tl & 15);
+        const bool in = p.sel_idx && t < tiles_c && j < p.kmax;
+        return in ? (int64_t)p.sel_idx[(int64_t)row * p.kmax + j] : 0;
+      };
+      auto fetch = [&](int it, int64_t i) -> bool {
+        const int s = it % C::kStages;
+        const int t = t0 + it;
+        if (p.sel_idx != nullptr && t < tiles_c) {
+          const int j = t * TN + tw + 4 * (tl & 15);
+          if (j >= n_c || i < 0 || i >= n_vis) i = -1;  // masked row: not fetched (zeroed later)
+          if (!wait_all(&empty[s], ((it / C::kStages) & 1) ^ 1, p, abort_flag)) return false;
+          if (it == C::kStages - 1 && !wait_all(qready, 0, p, abort_flag)) return false;
+          uint8_t* st = stages + s * C::kStageBytes;
+          constexpr int kUnits = D / 8;  // 16-byte units per row
+  #pragma unroll 4
+          for (int u = 0; u < TN / 4; ++u) {
+            const int64_t iu = __shfl_sync(0xffffffffu, i, u);
+            if (iu < 0) continue;
+            const int rr = tw + 4 * u;
+            const __nv_bfloat16* src = p.kv_c + ((int64_t)b * p.N_cap + iu) * D;
+  #pragma unroll
+            for (int h = 0; h < (kUnits + 31) / 32; ++h) {
+              const int unit = 32 * h + tl;
+              if (unit < kUnits) cp_async_16(st + tile_off(rr, 8 * unit), src + 8 * unit);
+            }
+          }
+          cp_async_arrive(&full[s]);
+        } else {
+          mbar_arrive(&full[s]);
+        }
+        return true;
+      };
+      constexpr int kAhead = C::kStages - 1;
+      bool fetch_ok = true;
+      {
+        int64_t ri[kAhead];
+  #pragma unroll
+        for (int u = 0; u < kAhead; ++u) ri[u] = u < ntile ? row_index(u) : 0;
+  #pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (u < ntile && fetch_ok) fetch_ok = fetch(u, ri[u]);
       }
-    }
-    cp_async_wait_all();  // no copy may still target shared memory at exit
+      int64_t nxt = kAhead < ntile ? row_index(kAhead) : 0;
+      for (int it = 0; it < ntile && fetch_ok; ++it) {
+        if (!transform(it)) break;
+        if (it + kAhead < ntile) {
+          const int64_t cur = nxt;
+          if (it + kAhead + 1 < ntile) nxt = row_index(it + kAhead + 1);
+          fetch_ok = fetch(it + kAhead, cur);
+        }
+      }
+      cp_async_wait_all();  // no copy may still target shared memory at exit
     }
   } else {
     // ------------------------------------------------- softmax / epilogue --
