@@ -343,12 +343,18 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
 // kernel has set itself up before the attention ends.
 template <int D>
 constexpr int kMergeParts = D / 128;
-// Groups of up to 16 are held to 72 registers: 8 rows of 128 heads are 1024 CTAs, and
-// seven on an SM take them in one wave (dense 8 x 8192 entries 37.6 us, 39.9 with 80
-// registers).  Larger groups merge few rows; there the registers of a lone CTA keep
-// all loads in flight (2 x 8192 entries 21.9 us, 22.3 with 128).
+// CTAs of the merge that share an SM, which limits its registers: the CTAs of a call
+// should be one wave, and its loads all be in flight.  8 rows of 128 heads (groups of
+// 16) are 1024 CTAs, seven an SM: dense 8 x 8192 entries 37.6 us, 39.9 with the 80
+// registers of six.  4 rows (18 splits, groups of 24) are 512, four an SM: 17.4 us,
+// 18.0 with five (96 registers), 19.4 with three (146); few CTAs at D = 128: 15.2 with
+// five, 15.6 with four.  Groups of 40 merge one or two rows: 21.7 us, 22.0 with 128
+// registers.  (bf16 caches; 4-bit ones 0.5 to 1.5 us less in the same order.)
+template <int D, int G>
+constexpr int kMergeCtas = G <= 16 ? 7 : G > 24 ? 1 : D == 128 ? 5 : 4;
+
 template <int D, int R, int G>
-__global__ void __launch_bounds__(128, G <= 16 ? 7 : 1)
+__global__ void __launch_bounds__(128, kMergeCtas<D, G>)
     mqa_combine_kernel(const Params p, int rows) {
   constexpr int kParts = kMergeParts<D>;
   extern __shared__ float wsm[];  // [4 warps][S] split weights
@@ -369,11 +375,11 @@ __global__ void __launch_bounds__(128, G <= 16 ? 7 : 1)
 }
 
 // The merge kernel for `splits` splits: the smallest group that takes them in
-// one round of loads (they go out with the (max, sum) pairs; a further round
-// costs 1.2 to 1.5 us), up to 40.  Whole calls at D = 512: 18 splits 17.3 us, in
-// groups of 16 18.6; 37 splits 22.3, in groups of 24 23.5; 66 splits 21.5, in
-// groups of 24 23.2.  At D = 128, few warps with cold code, groups of 40 lose
-// (66 splits 15.2 us, 14.5 in groups of 24).
+// one round of loads (they go out with the (max, sum) pairs), up to 40.  Whole
+// calls over a 4-bit cache at D = 512: 18 splits 15.9 us, in groups of 16 17.4; 37
+// splits 21.9, in groups of 24 22.5 and of 16 24.5; 66 splits 21.2, in groups of 16
+// 24.8.  At D = 128, few warps with cold code, groups of 40 lose (66 splits 14.6
+// us, 14.3 in groups of 24).
 template <int D, int R>
 auto merge_kernel(int splits) {
   if (splits <= 8) return mqa_combine_kernel<D, R, 8>;
