@@ -16,14 +16,16 @@
 // each TMEM sub-partition, so per CTA
 //     O    (64 heads x D fp32)         lane half 0, columns 0 .. D-1
 //     S    (64 heads x 64 fp32, x2)    lane half 1, columns 0 .. 127
-//     Qhat (64 heads x D bf16 pairs)   lane half 1, columns 128 .. 128+D/2-1
+//     Qhat (64 heads x D 16-bit pairs) lane half 1, columns 128 .. 128+D/2-1
 // (the A operand of S = Qhat K^T is read from TMEM in the same lane half as
 // the accumulator it feeds).  Per 64-entry tile:
-//   - contiguous tiles (dense entries, window tokens) arrive by TMA boxes
-//     issued by the producer warp; selected entries are gathered by the four
+//   - contiguous bf16 tiles (dense entries, window tokens) arrive by TMA boxes
+//     issued by the producer warp; selected bf16 entries are gathered by the four
 //     transform warps with 16-byte cp.async (two threads per row, a few
 //     tiles ahead), which keeps many more rows in flight than per-row TMA
-//     gathers; 128-byte swizzle either way, K = V = that tile;
+//     gathers; entries of a 4-bit cache, dense or selected, are loaded by eight
+//     transform warps a tile ahead and stored as fp16; 128-byte swizzle in every
+//     case, K = V = that tile;
 //   - transform warps zero masked rows and, for window tokens, compute
 //     1/rms(c_t), apply the KV gain and rotate the last R dims to the token
 //     position (compressed entries are stored already rotated to theirs);
@@ -33,7 +35,8 @@
 //   - softmax warps (two threads per head row, 32 columns each, through the
 //     16x32bx2 TMEM access) run an online softmax with lazy rescaling (O is
 //     rescaled in TMEM only when the running max grows by more than 8) and
-//     write P (bf16) to shared memory in the MMA's K-major layout.
+//     write P to shared memory in the MMA's K-major layout.
+// The products' operands (Qhat, P and the tile) are bf16, over a 4-bit cache fp16.
 // Splits of the KV list run on different CTAs; their (m, l, O) partials are
 // merged, with the sink folded in and the inverse RoPE applied, by
 // mqa_combine_kernel, which sets itself up while the attention still runs.
@@ -91,7 +94,7 @@ struct MCfg {
   static constexpr int kChunkBytes = TN * 128;     // one chunk of a tile
   static constexpr int kStageBytes = NC * kChunkBytes;
   static constexpr int kStages = D == 512 ? 3 : 4;
-  static constexpr int kPBytes = HC * TN * 2;      // P tile, bf16
+  static constexpr int kPBytes = HC * TN * 2;      // P tile, 16 bits a weight
   static constexpr uint32_t kHalf1 = 16u << 16;    // TMEM lane offset of lane half 1
   static constexpr int kQCol = 2 * TN;             // Qhat columns start (half 1)
   static constexpr uint32_t kAlloc = (D <= 256 && kQCol + D / 2 <= 256) ? 256 : 512;
@@ -148,7 +151,7 @@ CSA_DEV uint32_t tile_off(int r, int d) {
 // The 256 transform threads' share of an MXFP4 tile: thread tid holds block
 // blk (32 values) of rows row + u * kStep.  Eight neighbouring lanes hold two
 // blocks of four rows: 32 contiguous bytes of each (one sector), and eight
-// different 16-byte units of the swizzled bf16 rows (no bank conflict).
+// different 16-byte units of the swizzled 16-bit rows (no bank conflict).
 template <int D>
 struct MxTile {
   static constexpr int kBlk = D / kMxBlock;        // blocks per row
@@ -209,15 +212,6 @@ struct Partials {
   }
 };
 
-// Merge of the split partials of one (row, head) by kParts warps: fold in the
-// sink, normalise, apply the inverse rotation, store bf16 (and the
-// log-sum-exp).  Lane l owns dims [l*VPL, (l+1)*VPL) of its warp's part (VPL =
-// D/kParts/32), so the output leaves in coalesced 32-lane stores and the rotated
-// pairs (d, d + R/2) sit in lanes l and l ^ (R/2/VPL) of the last part.  The S (max, sum) pairs
-// become one weight per split (wsplit: S floats of this warp's shared
-// memory).  The first G splits' partials are loaded together with the
-// (max, sum) pairs, so that with S <= G the warp waits on one round of L2
-// reads; further groups of G follow one round each.
 // The rotation angle of pair `lane` at the row's position.
 template <int R>
 CSA_DEV float2 row_angle(const Params& p, int row, int lane) {
@@ -227,6 +221,15 @@ CSA_DEV float2 row_angle(const Params& p, int row, int lane) {
   return make_float2(sn, cs);
 }
 
+// Merge of the split partials of one (row, head) by kParts warps: fold in the
+// sink, normalise, apply the inverse rotation, store bf16 (and the
+// log-sum-exp).  Lane l owns dims [l*VPL, (l+1)*VPL) of its warp's part (VPL =
+// D/kParts/32), so the output leaves in coalesced 32-lane stores and the rotated
+// pairs (d, d + R/2) sit in lanes l and l ^ (R/2/VPL) of the last part.  The S
+// (max, sum) pairs become one weight per split (wsplit: S floats of this warp's
+// shared memory).  The first G splits' partials are loaded together with the
+// (max, sum) pairs, so that with S <= G the warp waits on one round of L2
+// reads; further groups of G follow one round each.
 template <int D, int R, int G, int kParts>
 CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, int part, int lane,
                         float* wsplit) {
@@ -896,7 +899,8 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       // The conversion competes with the softmax for issue slots and the
       // instruction cache: 8 sequences of 8192 entries took 81 us with 21
       // instructions a word of 8 codes on four warps, 47 on eight, 41 with the
-      // hardware's E2M1 conversion (about 10 a word); 39.5 from a bf16 cache.
+      // hardware's E2M1 conversion (about 10 a word).  The call now takes 39.0,
+      // 37.5 from a bf16 cache.
       using X = MxTile<D>;
       const X x(tid);
       const uint8_t* seq = p.kv4 + (int64_t)b * p.N_cap * mx_row_bytes(D);
@@ -1041,7 +1045,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
     const int hg = hg0 + hl;              // global head
     const bool head_ok = hg < p.H;
     const uint32_t lq = (uint32_t)(32 * q) << 16;  // lane base of this quarter
-    // Query prologue: qhat = RoPE(RMSNorm(q) * gamma_q), bf16 pairs -> TMEM.
+    // Query prologue: qhat = RoPE(RMSNorm(q) * gamma_q), 16-bit pairs -> TMEM.
     // Thread half hf holds dims [hf*D/2, hf*D/2 + D/2), i.e. Qhat columns
     // [hf*D/4, hf*D/4 + D/4): one 16x32bx2 store (second half at +D/4
     // columns) writes 64 dims of both halves.  The rotated dims (the last R)
@@ -1220,7 +1224,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       if (need) l_run *= fast_exp2(m_run - m_new);
       m_run = m_new;
       // P = 2^(logit - m) (times the window norm: V = norm * stored row) in
-      // bf16, into P buffer a: row hl, columns [32hf, 32hf+32), K-major with
+      // 16 bits, into P buffer a: row hl, columns [32hf, 32hf+32), K-major with
       // the 128-byte swizzle.
       const bool live = m_run != -INFINITY;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1444,7 +1448,7 @@ cudaError_t launch_impl(const MqaLaunch& a, cudaStream_t stream) {
   const int cps = a.H > HC ? 2 : 1;  // CTAs per (row, split)
   if (rows > 65535 || a.splits * cps > 65535) return cudaErrorInvalidConfiguration;
 
-  // Row-gather maps (one-row boxes) and 64-row box maps, 128-byte swizzle.
+  // Maps of 64-row boxes, 128-byte swizzle.
   CUtensorMap map_q, box_c, box_t;
   cudaError_t e = make_tmap_2d(&map_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                (uint64_t)rows * a.H, D, TN, 64, CU_TENSOR_MAP_SWIZZLE_128B);

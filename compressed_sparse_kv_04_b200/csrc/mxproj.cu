@@ -22,7 +22,8 @@
 // the MMAs that read its former scales have completed (its `full` barrier
 // follows its `empty` barrier).
 //
-// Two forms of one kernel (mx_gemm_kernel):
+// Up to 256 tokens, and for feature counts that are no multiple of 256, two forms
+// of one kernel (mx_gemm_kernel):
 //   - few tokens (T <= 128): weights are the MMA's M = 128 rows, tokens its N.
 //     The weights' bytes bound it.
 //   - more tokens: tokens are the M = 128 rows, weights N = 128, so that a
@@ -30,8 +31,8 @@
 //     quantises y in registers.
 // Either way K is split over the CTAs of a cluster where the tiles alone do
 // not fill the SMs (two CTAs each); the CTAs add their sums up over shared
-// memory, in the order of the splits, and finish the tile's tokens
-// and a second kernel on CTA pairs for many tokens (mx_pair_kernel).
+// memory, in the order of the splits, and finish the tile's tokens.
+// More tokens go to a second kernel, on CTA pairs (mx_pair_kernel).
 #include <algorithm>
 #include <atomic>
 
@@ -856,9 +857,9 @@ cudaError_t launch_mx_quantise(const void* x, int64_t ld, int64_t rows, int64_t 
                                void* scales, cudaStream_t stream) {
   const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((rows + 127) / 128));
   // Head mode where one wave of CTAs takes the rows (8 tokens: the whole
-  // projection 21.2 us a call in a stream, 24.7 without); with many CTAs, each
-  // of which would start with the wait, it costs more than it saves (4096 tokens:
-  // 413 us with, 377 without).
+  // projection 25.8 us a call among others, 28.6 without; in a graph 24.5 and 25.4);
+  // with many CTAs, each of which would start with the wait, it costs more than it
+  // saves (4096 tokens: 473 us with, 452 without; in a short graph 406 and 379).
   const int head = rows <= 128;
   return launch_pdl(mx_quantise_kernel, grid, dim3(256), 0, stream, 0, head,
                     static_cast<const uint8_t*>(x), ld * 2, rows, cols,
