@@ -1500,7 +1500,13 @@ cudaError_t launch_merge_impl(const MqaLaunch& a, cudaStream_t stream) {
   const int rows = a.B * a.Q;
   const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
-  return launch_pdl(merge_kernel<D, R>(a.splits), dim3(nblk), dim3(128), wsm, stream, 0, a.chained, p, rows);
+  auto kern = merge_kernel<D, R>(a.splits);
+  if (wsm > 48 * 1024) {  // more than 3072 splits
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)wsm);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(nblk), dim3(128), wsm, stream, 0, a.chained, p, rows);
 }
 
 }  // namespace

@@ -130,3 +130,36 @@ def test_context_split_partial_last_shard(orc):
     pos = (3 * 1024 + 100) * w.m + 2  # 3172 visible entries: shard 3 holds 100 of them
     r = run_split(w, G, 1, N, pos, seed=9)
     check(orc, w, r, pos, N)
+
+
+@pytest.mark.parametrize("d,R,splits", [(128, 32, 3073), (512, 64, 4096), (128, 0, 4096),
+                                        (512, 64, 3072)])
+def test_merge_of_thousands_of_splits(d, R, splits):
+    """Up to 4096 splits (their weights pass 48 KB of shared memory): against the
+    merge of the same partials in fp64, at position 0 (no rotation).  Every third
+    part is empty."""
+    B, H = 2, 3
+    g = torch.Generator(device=DEV).manual_seed(splits)
+    o = torch.randn(B, splits, H, d, generator=g, device=DEV).half()
+    ml = torch.empty(B, splits, 2, H, device=DEV)
+    ml[:, :, 0] = 4 * torch.randn(B, splits, H, generator=g, device=DEV)
+    ml[:, :, 1] = 1 + torch.rand(B, splits, H, generator=g, device=DEV)
+    ml[:, ::3, 0], ml[:, ::3, 1] = float("-inf"), 0.0
+    o[:, ::3] = float("nan")  # never read
+    sink = torch.randn(H, generator=g, device=DEV)
+    p = binding.make_params(B, d, H=H, window=0, rope_dim=R, m=4)
+    out = torch.empty(B, H, d, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(B, H, device=DEV)
+    binding.mqa_merge_partials(p, splits, o, ml, torch.zeros(B, dtype=torch.int64, device=DEV), sink,
+                               out, lse=lse)
+    torch.cuda.synchronize()
+    z = sink.double() / math.log(2)
+    w = ml[:, :, 1].double() * torch.exp2(ml[:, :, 0].double())
+    total = w.sum(1) + torch.exp2(z)
+    ref = (w[..., None] * o.double().nan_to_num(0.0)).sum(1) / total[..., None]
+    # fp32 sums of `splits` terms (2^-24 each, of the terms' magnitudes) and bf16's
+    # half step.
+    mag = (w[..., None] * o.double().nan_to_num(0.0).abs()).sum(1) / total[..., None]
+    assert ((out.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + mag * (splits + 64) * 2.0 ** -24).all()
+    want = torch.log(total)
+    assert ((lse.double() - want).abs() <= (splits + 64) * 2.0 ** -24 + want.abs() * 2.0 ** -22).all()
