@@ -1501,7 +1501,7 @@ cudaError_t launch_merge_impl(const MqaLaunch& a, cudaStream_t stream) {
   const unsigned nblk = (unsigned)(((int64_t)rows * a.H * kMergeParts<D> + 3) / 4);
   const size_t wsm = (size_t)4 * a.splits * sizeof(float);
   auto kern = merge_kernel<D, R>(a.splits);
-  if (wsm > 48 * 1024) {  // more than 3072 splits
+  if (wsm > 48 * 1024) {  // (what a launch gets without asking)
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)wsm);
     if (e != cudaSuccess) return e;

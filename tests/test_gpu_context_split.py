@@ -132,8 +132,8 @@ def test_context_split_partial_last_shard(orc):
     check(orc, w, r, pos, N)
 
 
-@pytest.mark.parametrize("d,R,splits", [(128, 32, 3073), (512, 64, 4096), (128, 0, 4096),
-                                        (512, 64, 3072)])
+@pytest.mark.parametrize("d,R,splits", [(128, 32, 3500), (512, 64, 4096), (128, 0, 4096),
+                                        (512, 64, 2500)])
 def test_merge_of_thousands_of_splits(d, R, splits):
     """Up to 4096 splits (their weights pass 48 KB of shared memory): against the
     merge of the same partials in fp64, at position 0 (no rotation).  Every third
