@@ -87,8 +87,9 @@ def _native():
         except ImportError as e:
             raise RuntimeError("_calls.so not found or not loadable; build it with "
                                "`python -m compressed_sparse_kv_04_b200.build`") from e
-        if m.built_for != build.calls_tag():
-            raise RuntimeError(f"_calls.so was built for {m.built_for}, this is "
+        built_for = getattr(m, "built_for", "an unknown torch")
+        if built_for != build.calls_tag():
+            raise RuntimeError(f"_calls.so was built for {built_for}, this is "
                                f"{build.calls_tag()}; build it again with "
                                "`python -m compressed_sparse_kv_04_b200.build`")
         m.bind(*(C.cast(f, C.c_void_p).value for f in (

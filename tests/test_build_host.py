@@ -1,8 +1,10 @@
 """What the build makes of what is installed, without compiling anything."""
 import os
+import types
 
 import pytest
 
+import compressed_sparse_kv_04_b200
 from compressed_sparse_kv_04_b200 import binding
 from compressed_sparse_kv_04_b200 import build as csa_build
 
@@ -90,4 +92,8 @@ def test_the_binding_refuses_native_calls_of_another_torch(monkeypatch):
     monkeypatch.setattr(binding, "_calls", None)
     monkeypatch.setattr(csa_build, "calls_tag", lambda: "torch 2.99")
     with pytest.raises(RuntimeError, match="built for .* this is torch 2.99"):
+        binding._native()
+    # A module from before modules said what they were built for.
+    monkeypatch.setattr(compressed_sparse_kv_04_b200, "_calls", types.SimpleNamespace())
+    with pytest.raises(RuntimeError, match="built for an unknown torch"):
         binding._native()
