@@ -266,6 +266,7 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
   // +inf sink, or nothing to attend
   const bool zero = (z == INFINITY && !isnan(M)) || M == -INFINITY;
   float L = 0.f;
+  bool none = false;
   if (!zero) {
     for (int s = lane; s < S; s += 32) {
       const float ms = s == lane ? m0 : src.maximum(s);
@@ -275,6 +276,8 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
       L += w;
     }
     L = warp_sum(L);
+    // (No weight at all: a zero row, also beside a NaN sink.)
+    none = L == 0.f;
     if (z2 != -INFINITY) L += exp2f(z2 - M);
   }
   __syncwarp();
@@ -303,7 +306,7 @@ CSA_DEV void merge_head(const Params& p, float z, float2 angle, int row, int h, 
         }
       }
     }
-    const float invL = 1.0f / L;
+    const float invL = none ? 0.f : 1.0f / L;
 #pragma unroll
     for (int e = 0; e < VPL; ++e) acc[e] *= invL;
     if constexpr (R > 0) {
@@ -1306,7 +1309,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
       bool zero = false;
       float ang_s = 0.f, ang_c = 1.f;
       if (p.fused) {
-        M = max_nan(m_run, z2);
+        M = max_nan(m_run, fmaxf(z2, -INFINITY));
         zero = (zs == INFINITY && !isnan(M)) || M == -INFINITY;
         if (!zero) {
           const float wm = m_run == -INFINITY ? 0.f : exp2f(m_run - M);
@@ -1386,7 +1389,7 @@ __global__ void __launch_bounds__(kBlockThreads<kMx>, 1)
         if (p.fused) {
           if (p.lse)
             p.lse[(int64_t)row * p.H + hg] =
-                zero ? (zs == INFINITY ? INFINITY : -INFINITY) : (M + log2f(L)) / LOG2E;
+                zero ? zs : (M + log2f(L)) / LOG2E;
         } else {
           pml[hg] = m_run;  // log2 domain
           pml[p.H + hg] = l_run;

@@ -334,8 +334,9 @@ csa_status lightning_index_topk_static(const csa_params* p, int Q, const uint8_t
  * RMSNorm is the KV norm, and they are stored rotated to their position
  * (i+1)*m-1); rotate-half pairing over the last rope_dim dims.  sink = -inf drops the sink; +inf
  * gives a zero output.  A row whose list holds a NaN logit (a NaN in the head's query, in an
- * attended entry or in a window token) is NaN, lse too, whatever the sink; a row with nothing to
- * attend is zero, its lse the sink.  Holds for every call that attends.
+ * attended entry or in a window token) is NaN, lse too, whatever the sink; so is one beside a
+ * NaN sink; a row with nothing to attend is zero, its lse the sink.  Holds for every call that
+ * attends.
  *
  *   q [B, H, d] bf16; pos_q [B] int64; kv_c [B, N_cap, d] bf16;
  *   topk_idx [B, k] int32, topk_cnt [B] int32 (entries must be < n_vis);

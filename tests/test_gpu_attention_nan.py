@@ -198,6 +198,28 @@ def test_masked_and_absent_rows_stay_out(mx, sparse, B):
     assert (out == 0).all() and torch.allclose(lse, e.sink.expand_as(lse), rtol=2.0 ** -22, atol=0)
 
 
+@BOTH
+@KIND
+@pytest.mark.parametrize("B", [2, ONE_SPLIT])
+@pytest.mark.parametrize("n_vis", [1, 65, 200])
+def test_a_nan_sink(mx, sparse, B, n_vis):
+    """A NaN sink makes its head NaN where there is something to attend; a row
+    with nothing to attend stays zero, its log-sum-exp the sink's, for one split
+    and for several."""
+    c = Case(mx, sparse, B, n_vis, d=128)
+    c.pos[0] = 1  # row 0: no entry is visible
+    c.cnt[0] = 0
+    before = c.run()
+    assert (before[0][0] == 0).all()
+    c.sink[5] = NAN
+    out, lse = c.run()
+    bad = torch.zeros(B, c.H, dtype=torch.bool, device=DEV)
+    bad[:, 5] = True
+    assert torch.isnan(lse[bad]).all()
+    assert (out[0] == 0).all() and torch.isnan(out[1:, 5]).all()
+    assert torch.equal(out[~bad], before[0][~bad]) and torch.equal(lse[~bad], before[1][~bad])
+
+
 def test_a_shard_of_a_split_context():
     """Partials of two shards merged: the one whose only selected entry is NaN
     is not taken for an empty one."""
